@@ -26,6 +26,10 @@ MAX_TOPK = 16
 MAX_MESSAGE_BYTES = 45056
 MAX_EXPERTS = 1 << 20
 SEND_MAX_EXPERTS = 4096
+FP32 = 2  # ll_moe_rms_norm: x in fp32
+ACT_NONE = 0
+ACT_SILU_MUL = 1
+GEMM_MAX_COLUMNS = 1 << 20
 REFUSAL_FLAG_WAIT = 1
 REFUSAL_COUNT_WAIT = 2
 RECV_READY = 0x100
@@ -63,6 +67,9 @@ _lib.ll_moe_combine_recv.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, 
 _lib.ll_moe_dispatch_recv.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _vp, _vp, _vp, _vp, _i, _vp,
                                       _vp]
 _lib.ll_moe_clean_signals.argtypes = [_vp, _i, _i, _i, _i, _i, _vp]
+_lib.ll_moe_expert_gemm.argtypes = [_i] * 7 + [_vp] * 8
+_lib.ll_moe_expert_gemm_w4.argtypes = [_i] * 6 + [_vp] * 7
+_lib.ll_moe_rms_norm.argtypes = [_i] * 4 + [ctypes.c_float] + [_vp] * 7
 _lib.ll_moe_diag_e4m3.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
 _lib.ll_moe_diag_e4m3_in_range.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
 _lib.ll_moe_diag_watch.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp]
@@ -73,6 +80,7 @@ _lib.ll_moe_status_string.argtypes = [_i]
 _lib.ll_moe_status_string.restype = ctypes.c_char_p
 for _f in ("ll_moe_layout_bytes", "ll_moe_layout_offsets", "ll_moe_dispatch",
            "ll_moe_combine", "ll_moe_combine_send", "ll_moe_combine_recv", "ll_moe_dispatch_recv",
+           "ll_moe_expert_gemm", "ll_moe_expert_gemm_w4", "ll_moe_rms_norm",
            "ll_moe_clean_signals", "ll_moe_diag_e4m3", "ll_moe_diag_e4m3_in_range",
            "ll_moe_diag_watch", "ll_moe_diag_stream",
            "ll_moe_diag_store_rows", "ll_moe_diag_gather_rows"):
@@ -97,6 +105,25 @@ def _ptr(a):
     if isinstance(a, int):
         return a
     return a.data_ptr()
+
+
+def _operand(call: str, a, device):
+    """Address of a contiguous tensor on `device` (or of a raw address): the
+    kernels take whole arrays, and run where the stream is."""
+    if a is None or isinstance(a, int):
+        return a
+    if not a.is_contiguous() or a.device != device:
+        raise LLMoEError(INVALID_ARGUMENT, call)
+    return a.data_ptr()
+
+
+def _operands(call: str, *tensors) -> list:
+    device = next((a.device for a in tensors if hasattr(a, "device")), None)
+    if device is not None:
+        import torch
+        if device.type != "cuda" or device.index != torch.cuda.current_device():
+            raise LLMoEError(INVALID_ARGUMENT, call)
+    return [_operand(call, a, device) for a in tensors]
 
 
 def _stream(s):
@@ -162,6 +189,34 @@ def ll_moe_dispatch_recv(layout, max_tokens: int, hidden: int, num_experts: int,
                                      expected, _ptr(payload), _ptr(scales), _ptr(src_tokens),
                                      _ptr(counts), max_spins, _ptr(status), _stream(stream)),
            "ll_moe_dispatch_recv")
+
+
+def ll_moe_expert_gemm(max_tokens: int, n: int, k: int, num_experts: int, dtype: int, act: int,
+                       out_dtype: int, a, a_scales, w, w_scales, counts, out, out_scales=None,
+                       stream=None) -> None:
+    """Products grouped by expert (bf16 or fp8), plain or gated. Tensors are
+    contiguous and on the current device."""
+    ptrs = _operands("ll_moe_expert_gemm", a, a_scales, w, w_scales, counts, out, out_scales)
+    _check(_lib.ll_moe_expert_gemm(max_tokens, n, k, num_experts, dtype, act, out_dtype, *ptrs,
+                                   _stream(stream)), "ll_moe_expert_gemm")
+
+
+def ll_moe_expert_gemm_w4(max_tokens: int, n: int, k: int, num_experts: int, group: int, act: int,
+                          a, w, w_scales, w_zeros, counts, out, stream=None) -> None:
+    """Products grouped by expert with 4-bit weights and a scale (and zero
+    point) a group. Tensors are contiguous and on the current device."""
+    ptrs = _operands("ll_moe_expert_gemm_w4", a, w, w_scales, w_zeros, counts, out)
+    _check(_lib.ll_moe_expert_gemm_w4(max_tokens, n, k, num_experts, group, act, *ptrs,
+                                      _stream(stream)), "ll_moe_expert_gemm_w4")
+
+
+def ll_moe_rms_norm(num_tokens: int, hidden: int, x_dtype: int, out_dtype: int, eps: float, x,
+                    residual, weight, residual_out, out, out_scales=None, stream=None) -> None:
+    """Root-mean-square norm of x plus the residual. Tensors are contiguous
+    and on the current device."""
+    ptrs = _operands("ll_moe_rms_norm", x, residual, weight, residual_out, out, out_scales)
+    _check(_lib.ll_moe_rms_norm(num_tokens, hidden, x_dtype, out_dtype, eps, *ptrs,
+                                _stream(stream)), "ll_moe_rms_norm")
 
 
 def ll_moe_clean_signals(layout, max_tokens: int, hidden: int, num_experts: int, dtype: int,

@@ -11,7 +11,7 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libllmoe.so")
 SOURCES = ["api.hip", "dispatch.hip", "combine.hip", "two_phase.hip", "receive.hip", "watch.hip",
-           "probe.hip"]
+           "probe.hip", "expert_api.hip", "gemm_few.hip", "norm.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -1,0 +1,123 @@
+// Products grouped by expert: what the kernels and the C ABI share.
+//
+// Expert e owns rows [e * max_tokens, (e + 1) * max_tokens) of the activations
+// and of the output and fills the first counts[e] of them, as the dispatch's
+// expert side leaves them. P = A W_e^T over those rows; the gated form takes
+// W_e of 2n rows and gives silu(P[:, :n]) * P[:, n:].
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace llmoe {
+
+enum : int { kWeightBf16 = 0, kWeightFp8 = 1, kWeightInt4 = 2 };
+
+struct GemmParams {
+  const uint8_t* a;         // bf16 or e4m3 [num_experts * max_tokens, k]
+  const float* a_scales;    // fp8: [num_experts * max_tokens, k / 128]
+  const uint8_t* w;         // [num_experts, n or 2n, k]; int4: k / 2 bytes a row
+  const void* w_scales;     // fp8: fp32 per 128 x 128; int4: bf16 per row and group
+  const uint8_t* w_zeros;   // int4: zero points as the scales, or null (8)
+  const int32_t* counts;    // [num_experts]
+  uint8_t* out;             // bf16 or e4m3 [num_experts * max_tokens, n]
+  float* out_scales;        // fp8 out: [num_experts * max_tokens, n / 128]
+  int max_tokens;
+  int num_experts;
+  int n;                    // output columns
+  int k;
+  int group;                // int4: weights along k that share a scale
+  int weight;               // kWeight...
+  int gated;                // silu(gate) * up
+  int out_fp8;
+};
+
+constexpr int kGemmMaxExperts = 4096;
+
+// Rows of the tile prefix below: one 32-bit word an expert and the total.
+inline uint32_t tile_prefix_bytes(int num_experts) {
+  return ((uint32_t)(num_experts + 1) * 4u + 15u) & ~15u;
+}
+
+// Row tiles before each expert: pre[e], e <= E, with ceil(rows / tile_rows)
+// tiles for an expert with `least` < rows <= `most` and none for the others
+// (they are another launch's). All THREADS threads call it; scan: one word a
+// wavefront.
+template <int THREADS>
+__device__ __forceinline__ void tile_prefix(const GemmParams& P, int tile_rows, int least, int most,
+                                            uint32_t* pre, uint32_t* scan) {
+  const int tid = threadIdx.x, lane = tid & 63, E = P.num_experts;
+  const int run = (E + THREADS - 1) / THREADS;
+  const int e0 = tid * run < E ? tid * run : E, e1 = e0 + run < E ? e0 + run : E;
+  uint32_t sum = 0;
+  for (int e = e0; e < e1; ++e) {
+    int c = P.counts[e];
+    c = c < P.max_tokens ? c : P.max_tokens;
+    const uint32_t t = c > least && c <= most ? (uint32_t)((c - 1) / tile_rows + 1) : 0u;
+    pre[e] = sum;
+    sum += t;
+  }
+  uint32_t incl = sum;
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) {
+    const uint32_t o = __shfl_up(incl, d, 64);
+    if (lane >= d) incl += o;
+  }
+  if (lane == 63) scan[tid / 64] = incl;
+  __syncthreads();
+  uint32_t base = incl - sum;
+  for (int w = 0; w < tid / 64; ++w) base += scan[w];
+  for (int e = e0; e < e1; ++e) pre[e] += base;
+  if (tid == THREADS - 1) pre[E] = base + sum;
+  __syncthreads();
+}
+
+// Expert of tile t < pre[E]: the largest e with pre[e] <= t. An expert
+// without tiles has pre[e] == pre[e + 1] and is never the answer.
+__device__ __forceinline__ int expert_of_tile(const uint32_t* pre, int E, uint32_t t) {
+  int lo = 0, hi = E - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) >> 1;
+    if (pre[mid] <= t) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t v4u __attribute__((ext_vector_type(4)));
+typedef uint32_t v2u __attribute__((ext_vector_type(2)));
+
+// fp32 -> bf16, nearest even, two at a time (gfx950's conversion
+// instruction; NaN stays NaN).
+__device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  const bf16x2 v = {(__bf16)lo, (__bf16)hi};
+  return __builtin_bit_cast(uint32_t, v);
+}
+
+// silu(g) * u in fp32. exp(-g) overflows to infinity for g below about -88:
+// the quotient is then -0, which is silu's limit.
+__device__ __forceinline__ float silu_mul(float g, float u) {
+  return g / (1.0f + __expf(-g)) * u;
+}
+
+// fp32 -> OCP e4m3 codes, four packed little-endian: nearest even, +-448 for
+// everything beyond and for the infinities, 0x7F for NaN.
+__device__ __forceinline__ uint32_t e4m3_pack4(float p0, float p1, float p2, float p3) {
+  const float c0 = __builtin_amdgcn_fmed3f(p0, -448.0f, 448.0f);
+  const float c1 = __builtin_amdgcn_fmed3f(p1, -448.0f, 448.0f);
+  const float c2 = __builtin_amdgcn_fmed3f(p2, -448.0f, 448.0f);
+  const float c3 = __builtin_amdgcn_fmed3f(p3, -448.0f, 448.0f);
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(c0, c1, 0, false);
+  w = __builtin_amdgcn_cvt_pk_fp8_f32(c2, c3, w, true);
+  const uint32_t m = (p0 != p0 ? 0xFFu : 0u) | (p1 != p1 ? 0xFF00u : 0u) |
+                     (p2 != p2 ? 0xFF0000u : 0u) | (p3 != p3 ? 0xFF000000u : 0u);
+  return ((uint32_t)w & ~m) | (0x7F7F7F7Fu & m);
+}
+
+hipError_t launch_gemm_few(const GemmParams& p, int most, hipStream_t stream);
+
+}  // namespace llmoe

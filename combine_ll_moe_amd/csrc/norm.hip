@@ -1,0 +1,152 @@
+// Root-mean-square norm of x plus the residual, with the new residual and an
+// output in bf16 or in e4m3 with a scale per 128 columns.
+//
+// Mathematics, for one row in fp32: h = x + residual; residual_out = h
+// rounded to bf16; y = h / sqrt(mean(h^2) + eps) * weight, taken from h
+// before that rounding; out = y in bf16, or codes e4m3(y * (448 / amax)) and
+// scales amax / 448 of each 128 columns, as the fp8 dispatch quantizes.
+//
+// Design: one workgroup a row (one wavefront for short rows, four rows a
+// workgroup), the row in registers from its one read to its one write: the
+// bytes moved are the floor's. A thread holds chunks of 8 columns, so 16
+// lanes hold the 128 columns that share a scale and reduce amax in four
+// steps.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "expert_gemm.h"
+#include "norm.h"
+
+namespace llmoe {
+namespace {
+
+__device__ __forceinline__ void unpack8(const v4u v, float (&f)[8]) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    f[2 * i] = __uint_as_float(v[i] << 16);
+    f[2 * i + 1] = __uint_as_float(v[i] & 0xFFFF0000u);
+  }
+}
+__device__ __forceinline__ v4u pack8(const float (&f)[8]) {
+  return v4u{bf16_pair(f[0], f[1]), bf16_pair(f[2], f[3]), bf16_pair(f[4], f[5]),
+             bf16_pair(f[6], f[7])};
+}
+
+// ROW: threads of a row; C: chunks of 8 columns a thread holds. A workgroup
+// of max(ROW, 256) threads takes rows side by side.
+template <int ROW, int C, bool X_FP32, bool OUT_FP8>
+__global__ void __launch_bounds__(ROW < 256 ? 256 : ROW) norm_kernel(const NormParams P) {
+  constexpr int BLOCK = ROW < 256 ? 256 : ROW;
+  __shared__ float part[BLOCK / 64];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int t0 = tid % ROW;
+  const int64_t row = (int64_t)blockIdx.x * (BLOCK / ROW) + tid / ROW;
+  const bool live = row < P.num_tokens;
+  const int chunks = P.hidden / 8;
+  const uint64_t base = (uint64_t)(live ? row : 0) * chunks;
+  float h[C][8];
+  v4u wt[C];
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = t0 + c * ROW;
+    if (live && i < chunks) {
+      wt[c] = reinterpret_cast<const v4u*>(P.weight)[i];
+      if constexpr (X_FP32) {
+        const f32x4* x = reinterpret_cast<const f32x4*>(P.x) + 2 * (base + i);
+        const f32x4 lo = x[0], hi = x[1];
+#pragma unroll
+        for (int j = 0; j < 4; ++j) h[c][j] = lo[j], h[c][4 + j] = hi[j];
+      } else {
+        unpack8(reinterpret_cast<const v4u*>(P.x)[base + i], h[c]);
+      }
+    } else {
+      wt[c] = v4u{0, 0, 0, 0};
+#pragma unroll
+      for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
+    }
+  }
+  if (P.residual) {
+#pragma unroll
+    for (int c = 0; c < C; ++c) {
+      const int i = t0 + c * ROW;
+      if (live && i < chunks) {
+        float r[8];
+        unpack8(reinterpret_cast<const v4u*>(P.residual)[base + i], r);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) h[c][j] += r[j];
+      }
+    }
+  }
+  float sum = 0.0f;
+#pragma unroll
+  for (int c = 0; c < C; ++c)
+#pragma unroll
+    for (int j = 0; j < 8; ++j) sum = __builtin_fmaf(h[c][j], h[c][j], sum);
+#pragma unroll
+  for (int d = 1; d < 64; d <<= 1) sum += __shfl_xor(sum, d, 64);
+  if constexpr (ROW > 64) {
+    if (lane == 0) part[tid / 64] = sum;
+    __syncthreads();
+    sum = 0.0f;
+#pragma unroll
+    for (int w = 0; w < ROW / 64; ++w) sum += part[w];
+  }
+  const float scale = 1.0f / sqrtf(sum / (float)P.hidden + P.eps);
+#pragma unroll
+  for (int c = 0; c < C; ++c) {
+    const int i = t0 + c * ROW;
+    const bool in = live && i < chunks;
+    if (P.residual_out && in) reinterpret_cast<v4u*>(P.residual_out)[base + i] = pack8(h[c]);
+    float w[8], y[8];
+    unpack8(wt[c], w);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) y[j] = h[c][j] * scale * w[j];
+    if constexpr (OUT_FP8) {
+      float amax = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));  // NaN is ignored
+#pragma unroll
+      for (int d = 1; d < 16; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
+      const float inv = amax > 0.0f ? 448.0f / amax : 0.0f;
+      if (in) {
+        reinterpret_cast<uint2*>(P.out)[base + i] =
+            make_uint2(e4m3_pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
+                       e4m3_pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
+        if ((i & 15) == 0)
+          P.out_scales[(base + i) / 16] = amax > 0.0f ? amax / 448.0f : 0.0f;
+      }
+    } else if (in) {
+      reinterpret_cast<v4u*>(P.out)[base + i] = pack8(y);
+    }
+  }
+}
+
+template <int ROW, int C, bool X_FP32>
+hipError_t launch(const NormParams& p, hipStream_t stream) {
+  constexpr int BLOCK = ROW < 256 ? 256 : ROW, ROWS = BLOCK / ROW;
+  const unsigned blocks = (unsigned)(((int64_t)p.num_tokens + ROWS - 1) / ROWS);
+  if (p.out_fp8) norm_kernel<ROW, C, X_FP32, true><<<blocks, BLOCK, 0, stream>>>(p);
+  else norm_kernel<ROW, C, X_FP32, false><<<blocks, BLOCK, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <bool X_FP32>
+hipError_t launch_x(const NormParams& p, hipStream_t stream) {
+  const int chunks = p.hidden / 8;
+  if (chunks <= 64) return launch<64, 1, X_FP32>(p, stream);
+  if (chunks <= 128) return launch<64, 2, X_FP32>(p, stream);
+  if (chunks <= 256) return launch<256, 1, X_FP32>(p, stream);
+  if (chunks <= 512) return launch<256, 2, X_FP32>(p, stream);
+  if (chunks <= 1024) return launch<256, 4, X_FP32>(p, stream);
+  if (chunks <= 2048) return launch<512, 4, X_FP32>(p, stream);
+  return launch<1024, 4, X_FP32>(p, stream);
+}
+
+}  // namespace
+
+hipError_t launch_norm(const NormParams& p, hipStream_t stream) {
+  if (p.num_tokens == 0) return hipSuccess;
+  return p.x_fp32 ? launch_x<true>(p, stream) : launch_x<false>(p, stream);
+}
+
+}  // namespace llmoe

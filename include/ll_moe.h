@@ -343,6 +343,101 @@ int ll_moe_clean_signals(void* layout, int max_tokens, int hidden,
                          int num_experts, int dtype, int parity,
                          hipStream_t stream);
 
+/*
+ * The operators around the expert side. Dispatch and combine move rows; what
+ * an expert computes from payload row to output row is two matrix products
+ * with a gated activation between them, and the rows that enter the dispatch
+ * come out of a norm. None of the pages defines these: the formulas here do.
+ *
+ * Rows stand as ll_moe_dispatch_recv leaves them: expert e owns rows
+ * [e * max_tokens, (e + 1) * max_tokens) of the activations and of the
+ * output, and its first counts[e] rows are filled (a count below 0 is taken
+ * as 0, one above max_tokens as max_tokens). The counts are read on the
+ * device when the call runs. Rows behind the count are neither read nor
+ * written, and weights of an expert without rows are not read. A product of
+ * a row depends on that row and the weights alone (a NaN or infinity stays
+ * in its row).
+ */
+#define LL_MOE_FP32 2                /* ll_moe_rms_norm: x in fp32 */
+#define LL_MOE_ACT_NONE 0
+#define LL_MOE_ACT_SILU_MUL 1        /* silu(gate) * up */
+#define LL_MOE_GEMM_MAX_COLUMNS (1 << 20)
+
+/*
+ * ll_moe_expert_gemm - products grouped by expert, bf16 or fp8.
+ * For every filled row r of expert e, with fp32 sums,
+ *   P[r, i] = sum over c < k of A[r, c] * W[e, i, c]
+ *   ACT_NONE:     out[r, i] = P[r, i], i < n (W_e has n rows)
+ *   ACT_SILU_MUL: out[r, i] = g / (1 + exp(-g)) * u with g = P[r, i],
+ *                 u = P[r, n + i] (W_e has 2n rows: n gate rows, n up rows).
+ *   dtype:      LL_MOE_BF16: a and w bf16, k % 8 == 0, n % 8 == 0.
+ *               LL_MOE_FP8_E4M3: a and w e4m3 codes, k % 128 == 0,
+ *               n % 16 == 0; A[r, c] = code * a_scales[r, c / 128],
+ *               W[e, i, c] = code * w_scales[e, i / 128, c / 128].
+ *   out_dtype:  LL_MOE_BF16 (one rounding of the fp32 value), or
+ *               LL_MOE_FP8_E4M3 (fp8 with ACT_SILU_MUL only, n % 128 == 0):
+ *               per row and 128 columns of the fp32 values, quantized as the
+ *               fp8 dispatch does (amax without NaN; codes of v * (448 /
+ *               amax); scale amax / 448; 0 and 0 when amax is 0). These are
+ *               the a and a_scales of a second product.
+ *   a:          device [num_experts * max_tokens, k], 16-byte aligned.
+ *   a_scales:   device fp32 [num_experts * max_tokens, k / 128] (fp8 only).
+ *   w:          device [num_experts, n or 2n, k], 16-byte aligned.
+ *   w_scales:   device fp32 [num_experts, ceil(rows of W / 128), k / 128]
+ *               (fp8 only; ignored for bf16, as a_scales is).
+ *   counts:     device int32 [num_experts].
+ *   out:        device [num_experts * max_tokens, n], 16-byte aligned.
+ *   out_scales: device fp32 [num_experts * max_tokens, n / 128] (fp8 out).
+ * Limits: num_experts <= LL_MOE_SEND_MAX_EXPERTS, num_experts * max_tokens <
+ * 2^31, n and k <= LL_MOE_GEMM_MAX_COLUMNS. Outputs may overlap neither an
+ * input nor each other. Enqueued on `stream`.
+ */
+int ll_moe_expert_gemm(int max_tokens, int n, int k, int num_experts, int dtype, int act,
+                       int out_dtype, const void* a, const float* a_scales, const void* w,
+                       const float* w_scales, const int32_t* counts, void* out,
+                       float* out_scales, hipStream_t stream);
+
+/*
+ * ll_moe_expert_gemm_w4 - the same products of bf16 rows with 4-bit weights,
+ *   W[e, i, c] = s[e, i, c / group] * (code[e, i, c] - z[e, i, c / group]).
+ *   group:    32, 64 or 128; k % group == 0, n % 8 == 0.
+ *   w:        device [num_experts, n or 2n, k / 2] bytes, 16-byte aligned: the
+ *             code (0..15) of an even c in the low half of byte c / 2, of the
+ *             odd c behind it in the high half.
+ *   w_scales: device bf16 [num_experts, n or 2n, k / group].
+ *   w_zeros:  device uint8 [num_experts, n or 2n, k / group], or NULL: 8.
+ *   out:      bf16.
+ * No weight is rounded: a group's codes are multiplied and summed in fp32 and
+ * the scale is applied to the sum. The sum is taken as sum((16 + code) * A) -
+ * (16 + z) * sum(A): a row that holds an infinity (or magnitudes whose 31-fold
+ * sums leave fp32's range) gives NaN. Everything else as ll_moe_expert_gemm.
+ */
+int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_experts, int group, int act,
+                          const void* a, const void* w, const void* w_scales,
+                          const uint8_t* w_zeros, const int32_t* counts, void* out,
+                          hipStream_t stream);
+
+/*
+ * ll_moe_rms_norm - root-mean-square norm of x plus the residual.
+ * For every row, in fp32: h = x + residual (h = x if residual is NULL);
+ * residual_out = h rounded to bf16 (unless NULL); y = h / sqrt(mean(h^2) +
+ * eps) * weight, from h before that rounding; out = y.
+ *   x_dtype:      LL_MOE_BF16, or LL_MOE_FP32 (ll_moe_combine's output).
+ *   out_dtype:    LL_MOE_BF16 (what the dispatch takes), or LL_MOE_FP8_E4M3:
+ *                 codes and scales as the fp8 dispatch quantizes, from the
+ *                 fp32 y (hidden % 128 == 0).
+ *   x, residual, residual_out, out: device [num_tokens, hidden], 16-byte
+ *                 aligned; residual and residual_out bf16, either may be NULL.
+ *   weight:       device bf16 [hidden], 16-byte aligned.
+ *   out_scales:   device fp32 [num_tokens, hidden / 128] (fp8 only).
+ *   num_tokens >= 0 (0 enqueues nothing), hidden % 8 == 0, hidden <= 32768,
+ *   eps finite and >= 0. residual_out may be residual itself; apart from that
+ *   outputs may overlap neither an input nor each other. Enqueued on `stream`.
+ */
+int ll_moe_rms_norm(int num_tokens, int hidden, int x_dtype, int out_dtype, float eps,
+                    const void* x, const void* residual, const void* weight,
+                    void* residual_out, void* out, float* out_scales, hipStream_t stream);
+
 /* Name of a status code (static string). */
 const char* ll_moe_status_string(int status);
 
