@@ -11,7 +11,8 @@ ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libllmoe.so")
 SOURCES = ["api.hip", "dispatch.hip", "combine.hip", "two_phase.hip", "receive.hip", "watch.hip",
-           "probe.hip", "expert_api.hip", "gemm_few.hip", "norm.hip"]
+           "probe.hip", "expert_api.hip", "gemm_few.hip",
+           "gemm_tile.hip", "norm.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -118,6 +118,8 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float p0, float p1, float p2, flo
   return ((uint32_t)w & ~m) | (0x7F7F7F7Fu & m);
 }
 
+// Rows of experts with at most `most` rows; of experts with more than `least`.
 hipError_t launch_gemm_few(const GemmParams& p, int most, hipStream_t stream);
+hipError_t launch_gemm_tile(const GemmParams& p, int least, hipStream_t stream);
 
 }  // namespace llmoe

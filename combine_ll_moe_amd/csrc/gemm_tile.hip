@@ -1,0 +1,342 @@
+// Products grouped by expert, for experts with many rows: tiles of 256 rows
+// and 256 weight rows on the matrix cores.
+//
+// Mathematics: as gemm_few.hip, P = A W^T over an expert's rows. fp8 with a
+// bf16 output: one 16x16x128 product per 128 columns, whose sum is scaled by
+// the activation's and the weight's scale and added up in fp32. The matrix
+// cores keep a sum of fp8 products to about 6e-6 of the products' magnitudes
+// (measured over 128 columns; a bf16 product to fp32's rounding); a bf16
+// output's own rounding is 2^-9 of it on average. The fp8 output comes with
+// fp32 scales, which would show it: there the codes become bf16, which holds
+// them exactly, and go through bf16 products at half the rate.
+//
+// Design: eight wavefronts, 4 x 2, each 64 rows by 128 weight rows. A k step
+// is 128 bytes of every row (64 bf16, 128 fp8): 64 KiB, copied from memory
+// straight into LDS while the step before it is multiplied, in two buffers.
+// A row's eight 16-byte chunks are permuted by the row's low bits, so that
+// the 16 lanes that read one chunk of 16 rows meet no bank twice; the copy
+// writes LDS in lane order, so it is the lanes' addresses that are permuted.
+// Rows behind the expert's count or behind n and columns behind k are outside
+// the buffer descriptors: zeros. A row quarter without rows is skipped; each
+// SIMD holds wavefronts of two quarters.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "expert_gemm.h"
+#include "kernels.h"
+
+namespace llmoe {
+namespace {
+
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr uint32_t kOutside = 0x7FFFFFF0u;
+constexpr int kTile = 256;            // rows of a tile, and weight rows
+constexpr int kStepBytes = 128;       // of a row in a k step
+constexpr int kHalf = kTile * kStepBytes;
+constexpr int kThreads = 512;
+
+__device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
+}
+
+typedef __attribute__((address_space(3))) uint8_t LdsByte;
+
+// What a wavefront copies of a k step: 32 rows of A and 32 of W, 8 rows an
+// instruction, lane l row l / 8 and slot l % 8 of it.
+struct Source {
+  Rsrc a, w;
+  uint32_t a_off, w_off;  // this lane's first row and chunk
+  uint32_t ld;            // row bytes
+  uint32_t chunk;         // byte of this lane's chunk in a step
+  uint32_t w_jump;        // bytes from W's tile row 128 as it would be to where it is
+};
+
+__device__ __forceinline__ void copy_step(const Source& s, int step, uint8_t* lds, int wave) {
+  const uint32_t at = (uint32_t)step * kStepBytes + s.chunk;
+  const bool in = at < s.ld;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const uint32_t rows = (uint32_t)i * 8 * s.ld;
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        s.a, (LdsByte*)(lds + (wave * 32 + i * 8) * kStepBytes), 16,
+        in ? (int)(s.a_off + rows + at) : (int)kOutside, 0, 0, 0);
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(
+        s.w, (LdsByte*)(lds + kHalf + (wave * 32 + i * 8) * kStepBytes), 16,
+        in ? (int)(s.w_off + rows + at) : (int)kOutside, 0, 0, 0);
+  }
+}
+
+// 16 bytes of chunk c of row r.
+__device__ __forceinline__ v4u chunk_of(const uint8_t* lds, int r, int c) {
+  return *reinterpret_cast<const v4u*>(lds + r * kStepBytes + ((c ^ (r & 7)) << 4));
+}
+
+// 16 codes as bf16, which holds e4m3 exactly.
+struct Bf16x16 {
+  bf16x8 lo, hi;
+};
+__device__ __forceinline__ Bf16x16 fp8_to_bf16(v4u v) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, false));
+    o[2 * i + 1] = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, true));
+  }
+  return {__builtin_bit_cast(bf16x8, v4u{o[0], o[1], o[2], o[3]}),
+          __builtin_bit_cast(bf16x8, v4u{o[4], o[5], o[6], o[7]})};
+}
+
+// LDS row of weight fragment f of column half wn. Gated tiles hold 128 gate
+// rows, then 128 up rows; a wavefront's fragments 0-3 are gate rows, 4-7 the
+// up rows of the same columns.
+template <bool GATED>
+__device__ __forceinline__ int frag_row(int wn, int f) {
+  return GATED ? (f < 4 ? 0 : 128) + wn * 64 + (f & 3) * 16 : wn * 128 + f * 16;
+}
+
+// One k step. acc[m][f]: lane l holds weight rows 4 (l / 16) + r of fragment
+// f for row l % 16 of row fragment m.
+template <int WEIGHT, bool GATED, bool OUT_FP8>
+__device__ __forceinline__ void multiply(const uint8_t* lds, int wm, int wn, const float (&as)[4],
+                                         const float (&ws)[3], int edge, f32x4 (&acc)[4][8]) {
+  const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
+  const uint8_t* la = lds;
+  const uint8_t* lw = lds + kHalf;
+  if constexpr (WEIGHT == kWeightBf16) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      v4u a[4], w[8];
+#pragma unroll
+      for (int m = 0; m < 4; ++m) a[m] = chunk_of(la, wm * 64 + m * 16 + lo, 4 * j + hi);
+#pragma unroll
+      for (int f = 0; f < 8; ++f) w[f] = chunk_of(lw, frag_row<GATED>(wn, f) + lo, 4 * j + hi);
+#pragma unroll
+      for (int f = 0; f < 8; ++f)
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              __builtin_bit_cast(bf16x8, w[f]), __builtin_bit_cast(bf16x8, a[m]), acc[m][f], 0, 0, 0);
+    }
+  } else {
+    v4u a[4][2];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) a[m][j] = chunk_of(la, wm * 64 + m * 16 + lo, 4 * j + hi);
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      v4u w[2];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) w[j] = chunk_of(lw, frag_row<GATED>(wn, f) + lo, 4 * j + hi);
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        f32x4 p = {0, 0, 0, 0};
+        if constexpr (OUT_FP8) {
+#pragma unroll
+          for (int j = 0; j < 2; ++j) {
+            const Bf16x16 wb = fp8_to_bf16(w[j]), ab = fp8_to_bf16(a[m][j]);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.lo, ab.lo, p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.hi, ab.hi, p, 0, 0, 0);
+          }
+        } else {
+          auto join = [](const v4u (&v)[2]) {
+            return i32x8{(int)v[0].x, (int)v[0].y, (int)v[0].z, (int)v[0].w,
+                         (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
+          };
+          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w), join(a[m]), p, 0, 0, 0, 0, 0, 0);
+        }
+        const float sc = as[m] * ws[!GATED || f < 4 ? 0 : f - 4 < edge ? 1 : 2];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[m][f][r] = __builtin_fmaf(sc, p[r], acc[m][f][r]);
+      }
+    }
+  }
+}
+
+template <int WEIGHT, bool GATED, bool OUT_FP8>
+__global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams P, int least) {
+  extern __shared__ __align__(16) uint8_t lds_raw[];
+  __shared__ uint32_t scan[kThreads / 64];
+  __shared__ __align__(16) uint8_t step0[2 * kHalf];
+  __shared__ __align__(16) uint8_t step1[2 * kHalf];
+  uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
+  tile_prefix<kThreads>(P, kTile, least, INT32_MAX, pre, scan);
+  const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  constexpr int COLS = GATED ? 128 : 256;  // output columns of a tile
+  const int across = (P.n + COLS - 1) / COLS;
+  const uint32_t row_tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
+  const uint64_t tiles = (uint64_t)row_tiles * across;
+  constexpr bool FP8 = WEIGHT == kWeightFp8;
+  const uint32_t ld = (uint32_t)P.k * (FP8 ? 1 : 2);
+  const int steps = (int)((ld + kStepBytes - 1) / kStepBytes);
+  const int kb = P.k / 128;
+
+  // Workgroups are dealt to the XCDs in turn; each XCD takes a run of the
+  // tiles, in which neighbours share rows or weights.
+  const uint64_t x = blockIdx.x % kXcds, per = gridDim.x / kXcds;
+  const uint64_t t0 = tiles * x / kXcds, t1 = tiles * (x + 1) / kXcds;
+  for (uint64_t t = t0 + blockIdx.x / kXcds; t < t1; t += per) {
+    // an expert's tiles: four tile columns at a time, all its row tiles
+    const int e = __builtin_amdgcn_readfirstlane(
+        expert_of_tile(pre, P.num_experts, (uint32_t)(t / across)));
+    const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e]);
+    const uint32_t down = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e + 1]) - first;
+    const uint64_t in_e = t - (uint64_t)first * across;
+    const int group = (int)(in_e / (4ull * down));
+    const int wide = across - 4 * group < 4 ? across - 4 * group : 4;
+    const int in_g = (int)(in_e - 4ull * down * group);
+    const int rt = in_g / wide, ct = 4 * group + in_g % wide;
+    int rows = P.counts[e];
+    rows = __builtin_amdgcn_readfirstlane(rows < P.max_tokens ? rows : P.max_tokens) - rt * kTile;
+    rows = rows < kTile ? rows : kTile;
+    const int64_t row0 = (int64_t)e * P.max_tokens + (int64_t)rt * kTile;
+    const int col0 = ct * COLS;
+    const int cols = P.n - col0 < COLS ? P.n - col0 : COLS;
+
+    Source s;
+    s.ld = ld;
+    s.a = rsrc_of(P.a + (uint64_t)row0 * ld, (uint32_t)rows * ld);
+    const uint64_t w_row = (uint64_t)e * (GATED ? 2 : 1) * P.n + col0;
+    // gated: wavefronts 4-7 copy the up rows
+    const bool up = GATED && wave >= 4;
+    s.w = rsrc_of(P.w + (w_row + (up ? P.n : 0)) * ld, (uint32_t)cols * ld);
+    const uint32_t r = (uint32_t)wave * 32 + (lane >> 3);
+    s.chunk = (uint32_t)((lane & 7) ^ (r & 7)) * 16;
+    s.a_off = r * ld;
+    s.w_off = (up ? r - 128 : r) * ld;
+
+    // fp8 scales: this lane's four rows, and the tile's weight blocks
+    const Rsrc ra = rsrc_of(FP8 ? P.a_scales + (uint64_t)row0 * kb : nullptr, FP8 ? (uint32_t)rows * kb * 4u : 0u);
+    const int wrows = (GATED ? 2 : 1) * P.n;
+    const float* wsp = FP8 ? static_cast<const float*>(P.w_scales) + (uint64_t)e * ((wrows + 127) / 128) * kb : nullptr;
+    // the weight blocks of this wavefront's fragments: 128 rows at a multiple
+    // of 128 (64 gate rows of them) lie in one; the 64 up rows start at any
+    // multiple of 16, and from fragment `edge` on they lie in the next
+    float as[2][4], ws[2][3];
+    const int b0 = GATED ? (col0 + wn * 64) / 128 : (col0 + wn * 128) / 128;
+    const int up0 = P.n + col0 + wn * 64;
+    const int b1 = GATED ? up0 / 128 : b0;
+    const int edge = ((b1 + 1) * 128 - up0) / 16;
+    auto scales = [&](int step, float (&av)[4], float (&wv)[3]) {
+      if constexpr (FP8) {
+#pragma unroll
+        for (int m = 0; m < 4; ++m)
+          av[m] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
+              ra, (int)(4u * ((uint32_t)(wm * 64 + m * 16 + lo) * kb + step)), 0, 0));
+        const int last = (wrows + 127) / 128 - 1;
+        wv[0] = wsp[(uint64_t)(b0 < last ? b0 : last) * kb + step];
+        if constexpr (GATED) {
+          wv[1] = wsp[(uint64_t)(b1 < last ? b1 : last) * kb + step];
+          wv[2] = wsp[(uint64_t)(b1 < last ? b1 + 1 : last) * kb + step];
+        }
+      }
+    };
+
+    f32x4 acc[4][8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int f = 0; f < 8; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
+    const bool busy = wm * 64 < rows;
+
+    copy_step(s, 0, step0, wave);
+    scales(0, as[0], ws[0]);
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    for (int k = 0; k < steps; k += 2) {
+      if (k + 1 < steps) {
+        copy_step(s, k + 1, step1, wave);
+        scales(k + 1, as[1], ws[1]);
+      }
+      if (busy) multiply<WEIGHT, GATED, OUT_FP8>(step0, wm, wn, as[0], ws[0], edge, acc);
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      __syncthreads();
+      if (k + 1 >= steps) break;
+      if (k + 2 < steps) {
+        copy_step(s, k + 2, step0, wave);
+        scales(k + 2, as[0], ws[0]);
+      }
+      if (busy) multiply<WEIGHT, GATED, OUT_FP8>(step1, wm, wn, as[1], ws[1], edge, acc);
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      __syncthreads();
+    }
+
+    // outputs: a lane's four consecutive columns of one row
+    constexpr int F = GATED ? 4 : 8;
+    float* most = reinterpret_cast<float*>(step0);  // fp8: amax of a row's half, [256][2]
+    if constexpr (GATED) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int f = 0; f < 4; ++f)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) acc[m][f][q] = silu_mul(acc[m][f][q], acc[m][f + 4][q]);
+    }
+    if constexpr (OUT_FP8) {
+#pragma unroll
+      for (int m = 0; m < 4; ++m) {
+        float v = 0.0f;
+#pragma unroll
+        for (int f = 0; f < F; ++f)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v = fmaxf(v, fabsf(acc[m][f][q]));  // NaN is ignored
+        v = fmaxf(v, __shfl_xor(v, 16, 64));
+        v = fmaxf(v, __shfl_xor(v, 32, 64));
+        if (hi == 0) most[(wm * 64 + m * 16 + lo) * 2 + wn] = v;
+      }
+      __syncthreads();
+    }
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+      const int row = wm * 64 + m * 16 + lo;
+      if (row < rows) {
+        const uint64_t orow = (uint64_t)(row0 + row);
+        float inv = 0.0f;
+        if constexpr (OUT_FP8) {
+          const float amax = fmaxf(most[row * 2], most[row * 2 + 1]);
+          inv = amax > 0.0f ? 448.0f / amax : 0.0f;
+          if (wn == 0 && hi == 0)
+            P.out_scales[orow * (P.n / 128) + ct] = amax > 0.0f ? amax / 448.0f : 0.0f;
+        }
+#pragma unroll
+        for (int f = 0; f < F; ++f) {
+          const int col = wn * F * 16 + f * 16 + 4 * hi;
+          const f32x4 v = acc[m][f];
+          if (col < cols) {
+            if constexpr (OUT_FP8)
+              *reinterpret_cast<uint32_t*>(P.out + orow * P.n + col0 + col) =
+                  e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
+            else
+              *reinterpret_cast<uint2*>(P.out + 2 * (orow * P.n + col0 + col)) =
+                  make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+          }
+        }
+      }
+    }
+    __syncthreads();  // the buffers are free for the next tile
+  }
+}
+
+template <int WEIGHT, bool GATED, bool OUT_FP8>
+hipError_t launch(const GemmParams& p, int least, hipStream_t stream) {
+  gemm_tile_kernel<WEIGHT, GATED, OUT_FP8>
+      <<<256, kThreads, tile_prefix_bytes(p.num_experts), stream>>>(p, least);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_gemm_tile(const GemmParams& p, int least, hipStream_t stream) {
+  if (p.weight == kWeightFp8) {
+    if (p.out_fp8) return launch<kWeightFp8, true, true>(p, least, stream);
+    return p.gated ? launch<kWeightFp8, true, false>(p, least, stream)
+                   : launch<kWeightFp8, false, false>(p, least, stream);
+  }
+  return p.gated ? launch<kWeightBf16, true, false>(p, least, stream)
+                 : launch<kWeightBf16, false, false>(p, least, stream);
+}
+
+}  // namespace llmoe
