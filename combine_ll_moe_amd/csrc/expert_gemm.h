@@ -34,15 +34,16 @@ struct GemmParams {
 
 constexpr int kGemmMaxExperts = 4096;
 
-// Rows of the tile prefix below: one 32-bit word an expert and the total.
+// LDS of the tile prefix below: a word an expert and the total, then the
+// experts' rows.
 inline uint32_t tile_prefix_bytes(int num_experts) {
-  return ((uint32_t)(num_experts + 1) * 4u + 15u) & ~15u;
+  return ((uint32_t)(2 * num_experts + 1) * 4u + 15u) & ~15u;
 }
 
 // Row tiles before each expert: pre[e], e <= E, with ceil(rows / tile_rows)
 // tiles for an expert with `least` < rows <= `most` and none for the others
-// (they are another launch's). All THREADS threads call it; scan: one word a
-// wavefront.
+// (they are another launch's); the rows of each expert behind them. All
+// THREADS threads call it; scan: one word a wavefront.
 template <int THREADS>
 __device__ __forceinline__ void tile_prefix(const GemmParams& P, int tile_rows, int least, int most,
                                             uint32_t* pre, uint32_t* scan) {
@@ -55,6 +56,7 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, int tile_rows, 
     c = c < P.max_tokens ? c : P.max_tokens;
     const uint32_t t = c > least && c <= most ? (uint32_t)((c - 1) / tile_rows + 1) : 0u;
     pre[e] = sum;
+    pre[E + 1 + e] = (uint32_t)c;
     sum += t;
   }
   uint32_t incl = sum;
@@ -96,6 +98,24 @@ __device__ __forceinline__ uint32_t bf16_pair(float lo, float hi) {
   typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
   const bf16x2 v = {(__bf16)lo, (__bf16)hi};
   return __builtin_bit_cast(uint32_t, v);
+}
+
+// 16 e4m3 codes as bf16, which holds them exactly.
+struct Bf16x16 {
+  bf16x8 lo, hi;
+};
+__device__ __forceinline__ Bf16x16 fp8_to_bf16(v4u v) {
+  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+  uint32_t o[8];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    o[2 * i] = __builtin_bit_cast(
+        uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, false));
+    o[2 * i + 1] = __builtin_bit_cast(
+        uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, true));
+  }
+  return {__builtin_bit_cast(bf16x8, v4u{o[0], o[1], o[2], o[3]}),
+          __builtin_bit_cast(bf16x8, v4u{o[4], o[5], o[6], o[7]})};
 }
 
 // silu(g) * u in fp32. exp(-g) overflows to infinity for g below about -88:

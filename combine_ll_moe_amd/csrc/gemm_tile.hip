@@ -71,22 +71,6 @@ __device__ __forceinline__ v4u chunk_of(const uint8_t* lds, int r, int c) {
   return *reinterpret_cast<const v4u*>(lds + r * kStepBytes + ((c ^ (r & 7)) << 4));
 }
 
-// 16 codes as bf16, which holds e4m3 exactly.
-struct Bf16x16 {
-  bf16x8 lo, hi;
-};
-__device__ __forceinline__ Bf16x16 fp8_to_bf16(v4u v) {
-  typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
-  uint32_t o[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    o[2 * i] = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, false));
-    o[2 * i + 1] = __builtin_bit_cast(uint32_t, (bf16x2)__builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[i], 1.0f, true));
-  }
-  return {__builtin_bit_cast(bf16x8, v4u{o[0], o[1], o[2], o[3]}),
-          __builtin_bit_cast(bf16x8, v4u{o[4], o[5], o[6], o[7]})};
-}
-
 // LDS row of weight fragment f of column half wn. Gated tiles hold 128 gate
 // rows, then 128 up rows; a wavefront's fragments 0-3 are gate rows, 4-7 the
 // up rows of the same columns.
@@ -189,8 +173,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
     const int wide = across - 4 * group < 4 ? across - 4 * group : 4;
     const int in_g = (int)(in_e - 4ull * down * group);
     const int rt = in_g / wide, ct = 4 * group + in_g % wide;
-    int rows = P.counts[e];
-    rows = __builtin_amdgcn_readfirstlane(rows < P.max_tokens ? rows : P.max_tokens) - rt * kTile;
+    int rows = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + e]) - rt * kTile;
     rows = rows < kTile ? rows : kTile;
     const int64_t row0 = (int64_t)e * P.max_tokens + (int64_t)rt * kTile;
     const int col0 = ct * COLS;
