@@ -118,6 +118,7 @@ extern "C" int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_exper
   const bool gated = act == LL_MOE_ACT_SILU_MUL;
   const uint64_t rows = (uint64_t)num_experts * max_tokens, rows_w = gated ? 2 * (uint64_t)n : n;
   const uint64_t groups = num_experts * rows_w * (k / group);
+  if (rows_w * (k / group) >= 1ull << 30) return LL_MOE_INVALID_ARGUMENT;  // 32-bit offsets of the scales
   const Span reads[] = {{a, rows * k * 2},
                         {w, num_experts * rows_w * k / 2},
                         {w_scales, groups * 2},

@@ -37,6 +37,10 @@ typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset behind every descriptor's range
 constexpr int kFewRows = 64;      // rows of a tile
 constexpr int kFewFrags = 4;      // weight strips a wavefront holds at once
+constexpr int kFewWaves = 4;      // of a workgroup
+// From this many strips a wavefront (in units of what it holds at once) on,
+// the list is long.
+constexpr int kFewLong = 4;
 constexpr int kPartLd = kFewFrags * 16 + 4;  // floats of a row of partial sums, at most
 
 __device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
@@ -44,6 +48,10 @@ __device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
 }
 __device__ __forceinline__ v4u load16(Rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
+}
+
+__device__ __forceinline__ float load_f32(Rsrc r, uint32_t off) {
+  return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
 }
 
 // One 16-row strip list of one expert and row tile.
@@ -140,11 +148,12 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
     rw[f] = rsrc_of(w + (uint64_t)strip_row<NF, GATED>(P, it.strip, f) * ld,
                     (uint32_t)strip_rows<NF, GATED>(P, it, f) * ld);
   // Scales: lane quarter q loads row fragment q's (lane's row) and strip q's.
-  const int arow = (MF > 1 ? hi % MF : 0) * 16 + lo;
-  const float* as_p = it.a_scales + (uint64_t)(arow < it.rows ? arow : it.rows - 1) * chunks;
-  const int wblock = strip_row<NF, GATED>(P, it.strip, hi % NF) / 128;
-  const float* ws_p = static_cast<const float*>(P.w_scales) +
-                      ((uint64_t)it.e * blocks + (wblock < blocks ? wblock : blocks - 1)) * chunks;
+  // Those of a chunk behind k are zeros.
+  const Rsrc rs = rsrc_of(it.a_scales, (uint32_t)it.rows * chunks * 4u);
+  const Rsrc rws = rsrc_of(static_cast<const float*>(P.w_scales) + (uint64_t)it.e * blocks * chunks,
+                           (uint32_t)blocks * chunks * 4u);
+  const uint32_t as_at = 4u * ((MF > 1 ? hi % MF : 0) * 16 + lo) * chunks;
+  const uint32_t ws_at = 4u * (strip_row<NF, GATED>(P, it.strip, hi % NF) / 128) * chunks;
   const uint32_t row = lo * ld, col = 16u * hi;
   v4u wb[D][NF][2], ab[D][MF][2];
   float as[D], sw[D];
@@ -158,8 +167,8 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
 #pragma unroll
       for (int m = 0; m < MF; ++m) ab[s][m][j] = load16(ra, in ? off + 64u * j + m * 16u * ld : kOutside);
     }
-    as[s] = as_p[in ? c : chunks - 1];  // a chunk behind k is zeros: any scale does
-    sw[s] = ws_p[in ? c : chunks - 1];
+    as[s] = load_f32(rs, in ? as_at + 4u * c : kOutside);
+    sw[s] = load_f32(rws, in ? ws_at + 4u * c : kOutside);
   };
 #pragma unroll
   for (int s = 0; s < D; ++s) load(s, kw + s * WK);
@@ -183,7 +192,6 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
           }
         }
       }
-      const bool in = c + s * WK < chunks;  // else 0 * a scale that may be NaN
 #pragma unroll
       for (int m = 0; m < MF; ++m) {
         const float av = MF > 1 ? __shfl(as[s], m * 16 + lo, 64) : as[s];
@@ -191,7 +199,7 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
         for (int f = 0; f < NF; ++f) {
           const float wv = __builtin_bit_cast(
               float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw[s]), f * 16));
-          const float sc = in ? av * wv : 0.0f;
+          const float sc = av * wv;
 #pragma unroll
           for (int r = 0; r < 4; ++r) acc[m][f][r] = __builtin_fmaf(sc, p[m][f][r], acc[m][f][r]);
         }
@@ -201,10 +209,18 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
   }
 }
 
-// Eight codes of a word as bf16 16 + c, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w) {
-  const v4u v = {((w << 3) & 0x00780078u) | 0x41804180u, ((w >> 1) & 0x00780078u) | 0x41804180u,
-                 ((w >> 5) & 0x00780078u) | 0x41804180u, ((w >> 9) & 0x00780078u) | 0x41804180u};
+// Eight codes of a word as bf16 16 + c, in the order 0 4 1 5 2 6 3 7. The two
+// constants come in registers: an and-or takes no literals, and with literals
+// each would be two instructions.
+struct CodeMasks {
+  uint32_t keep, base;
+  __device__ CodeMasks() : keep(0x00780078u), base(0x41804180u) {
+    asm("" : "+s"(keep), "+v"(base));
+  }
+};
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w, const CodeMasks& c) {
+  const v4u v = {((w << 3) & c.keep) | c.base, ((w >> 1) & c.keep) | c.base,
+                 ((w >> 5) & c.keep) | c.base, ((w >> 9) & c.keep) | c.base};
   return __builtin_bit_cast(bf16x8, v);
 }
 // Eight bf16 of A in that order.
@@ -214,133 +230,397 @@ __device__ __forceinline__ bf16x8 a_like_codes(v4u a) {
   return __builtin_bit_cast(bf16x8, v);
 }
 
-// G / 32 products of 32 columns cover a group; lane quarter g holds columns
-// [g G / 4, (g + 1) G / 4) of it, so that its codes are G / 8 bytes in a row.
+// Four words of four lane quarters transposed: word j of quarter q becomes
+// word q of quarter j.
+__device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
+  auto swap32 = [](uint32_t& a, uint32_t& b) {
+    const auto v = __builtin_amdgcn_permlane32_swap(a, b, false, false);
+    a = v[0];
+    b = v[1];
+  };
+  auto swap16 = [](uint32_t& a, uint32_t& b) {
+    const auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
+    a = v[0];
+    b = v[1];
+  };
+  swap32(w[0], w[2]);
+  swap32(w[1], w[3]);
+  swap16(w[0], w[1]);
+  swap16(w[2], w[3]);
+}
+
+// A chunk is 128 columns: 16 bytes of codes a lane, quarter q the columns
+// [32 q, 32 q + 32). Transposed among the quarters, word j of quarter q holds
+// columns 32 j + 8 q and on: product j covers columns [32 j, 32 j + 32), which
+// lie in one group, and A's fragments are read as they stand.
 template <int MF, int NF, bool GATED, int G>
 __device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, int kw, int WK,
                                          f32x4 (&acc)[MF][NF]) {
   constexpr int D = MF == 4 ? 1 : MF == 2 ? 2 : 3;
-  constexpr int J = G / 32;
+  constexpr int GROUPS = 128 / G;  // of a chunk
   const int lane = threadIdx.x & 63;
   const uint32_t lda = 2u * (uint32_t)P.k, ldw = (uint32_t)P.k / 2;
-  const int groups = P.k / G;
+  const int groups = P.k / G, chunks = (P.k + 127) / 128;
   const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * lda);
   Rsrc rw[NF];
   const int rows_w = (GATED ? 2 : 1) * P.n;
-  const bool zeros = P.w_zeros != nullptr;
 #pragma unroll
   for (int f = 0; f < NF; ++f)
     rw[f] = rsrc_of(P.w + ((uint64_t)it.e * rows_w + strip_row<NF, GATED>(P, it.strip, f)) * ldw,
                     (uint32_t)strip_rows<NF, GATED>(P, it, f) * ldw);
-  const uint32_t r = lane & 15, g = lane >> 4;
-  // Lane quarter q loads strip q's scales and zero points.
-  const int srow = strip_row<NF, GATED>(P, it.strip, (int)g % NF) + (int)r;
-  const uint64_t sat = ((uint64_t)it.e * rows_w + (srow < rows_w ? srow : rows_w - 1)) * groups;
-  const uint16_t* s_p = static_cast<const uint16_t*>(P.w_scales) + sat;
-  const uint8_t* z_p = P.w_zeros + sat;
-  uint32_t wb[D][NF][J], sb[D], zb[D];
-  v4u ab[D][MF][J];
+  const uint32_t lo = lane & 15, hi = lane >> 4;
+  // Lane quarter q loads strip q's scales and zero points; those of a group
+  // behind k are zeros. Without zero points their descriptor is empty.
+  const uint32_t values = (uint32_t)rows_w * groups;
+  const Rsrc rs = rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)it.e * values, 2 * values);
+  const Rsrc rz = rsrc_of(P.w_zeros + (P.w_zeros ? (uint64_t)it.e * values : 0), P.w_zeros ? values : 0u);
+  const float z_none = P.w_zeros ? 16.0f : 24.0f;
+  const uint32_t s_at = (uint32_t)(strip_row<NF, GATED>(P, it.strip, (int)hi % NF) + (int)lo) * groups;
+  v4u wb[D][NF], ab[D][MF][4];
+  uint32_t sb[D][GROUPS], zb[D][GROUPS];
   auto load = [&](int s, int c) {
-    const bool in = c < groups;
-    const uint32_t woff = in ? r * ldw + (uint32_t)c * (G / 2) + g * (G / 8) : kOutside;
+    const uint32_t wat = 64u * (uint32_t)c + 16u * hi;
+    const uint32_t woff = c < chunks && wat < ldw ? lo * ldw + wat : kOutside;
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      if constexpr (J == 4) {
-        const v4u v = load16(rw[f], woff);
-        wb[s][f][0] = v.x; wb[s][f][1] = v.y; wb[s][f][2] = v.z; wb[s][f][3] = v.w;
-      } else if constexpr (J == 2) {
-        const v2u v = __builtin_amdgcn_raw_buffer_load_b64(rw[f], (int)woff, 0, 0);
-        wb[s][f][0] = v.x; wb[s][f][1] = v.y;
-      } else {
-        wb[s][f][0] = __builtin_amdgcn_raw_buffer_load_b32(rw[f], (int)woff, 0, 0);
-      }
+    for (int f = 0; f < NF; ++f) wb[s][f] = load16(rw[f], woff);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const uint32_t at = 256u * (uint32_t)c + 64u * j + 16u * hi;
+      const bool in = c < chunks && at < lda;
+#pragma unroll
+      for (int m = 0; m < MF; ++m)
+        ab[s][m][j] = load16(ra, in ? (lo + m * 16u) * lda + at : kOutside);
     }
-    const uint32_t aoff = in ? r * lda + (uint32_t)c * (2 * G) + g * (G / 2) : kOutside;
 #pragma unroll
-    for (int m = 0; m < MF; ++m)
-#pragma unroll
-      for (int j = 0; j < J; ++j)
-        ab[s][m][j] = load16(ra, in ? aoff + m * 16u * lda + 16u * j : kOutside);
-    const int at = in ? c : groups - 1;  // a group behind k is zeros: any scale does
-    sb[s] = s_p[at];
-    zb[s] = zeros ? z_p[at] : 8u;
+    for (int u = 0; u < GROUPS; ++u) {
+      const int g = c * GROUPS + u;
+      const uint32_t at = s_at + (uint32_t)g;
+      sb[s][u] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(g < groups ? 2 * at : kOutside), 0, 0);
+      zb[s][u] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)(g < groups ? at : kOutside), 0, 0);
+    }
   };
   const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
+  const CodeMasks masks;
 #pragma unroll
   for (int s = 0; s < D; ++s) load(s, kw + s * WK);
-  for (int c = kw; c < groups; c += D * WK) {
+  for (int c = kw; c < chunks; c += D * WK) {
 #pragma unroll
     for (int s = 0; s < D; ++s) {
       const f32x4 zero = {0, 0, 0, 0};
-      bf16x8 x[MF][J];
-      f32x4 sum[MF];
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        sum[m] = zero;
-#pragma unroll
-        for (int j = 0; j < J; ++j) {
-          x[m][j] = a_like_codes(ab[s][m][j]);
-          sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][j], ones, sum[m], 0, 0, 0);
-        }
-      }
-      const float scale = __uint_as_float(sb[s] << 16), zero_at = 16.0f + (float)zb[s];
+      uint32_t wt[NF][4];
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
-        f32x4 p[MF];
+        wt[f][0] = wb[s][f].x, wt[f][1] = wb[s][f].y, wt[f][2] = wb[s][f].z, wt[f][3] = wb[s][f].w;
+        transpose_quarters(wt[f]);
+      }
 #pragma unroll
-        for (int m = 0; m < MF; ++m) p[m] = zero;
+      for (int u = 0; u < GROUPS; ++u) {
+        const float scale = __uint_as_float(sb[s][u] << 16);
+        const float zero_at = z_none + (float)zb[s][u];
+        f32x4 p[MF][NF], sum[MF];
 #pragma unroll
-        for (int j = 0; j < J; ++j) {
-          const bf16x8 wf = codes_bf16(wb[s][f][j]);
+        for (int j = u * (G / 32); j < (u + 1) * (G / 32); ++j) {
+          const bool start = j == u * (G / 32);
+          bf16x8 x[MF];
+#pragma unroll
+          for (int m = 0; m < MF; ++m) {
+            x[m] = a_like_codes(ab[s][m][j]);
+            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m], ones, start ? zero : sum[m], 0, 0, 0);
+          }
+#pragma unroll
+          for (int f = 0; f < NF; ++f) {
+            const bf16x8 wf = codes_bf16(wt[f][j], masks);
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+              p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m], wf, start ? zero : p[m][f], 0, 0, 0);
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < NF; ++f) {
+          const float sc = __shfl(scale, f * 16 + (int)lo, 64);
+          const float off = __shfl(zero_at, f * 16 + (int)lo, 64);
 #pragma unroll
           for (int m = 0; m < MF; ++m)
-            p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m][j], wf, p[m], 0, 0, 0);
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][f][r] = __builtin_fmaf(sc, __builtin_fmaf(-off, sum[m][r], p[m][f][r]), acc[m][f][r]);
         }
-        const bool in = c + s * WK < groups;  // else 0 * a scale that may be NaN
-        const float sc = in ? __shfl(scale, f * 16 + (int)r, 64) : 0.0f;
-        const float off = __shfl(zero_at, f * 16 + (int)r, 64);
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-#pragma unroll
-          for (int r2 = 0; r2 < 4; ++r2)
-            acc[m][f][r2] = __builtin_fmaf(sc, __builtin_fmaf(-off, sum[m][r2], p[m][r2]), acc[m][f][r2]);
+        __builtin_amdgcn_sched_barrier(0);  // groups in turn: their registers do not add up
       }
       load(s, c + (s + D) * WK);
     }
   }
 }
 
-// What the wavefronts of a workgroup do with items: WN lists of strips beside
-// each other, k split WK ways; or (WK = 0) each wavefront alone with its own.
-// Sums first, then, 16 rows at a time, the partial sums meet in LDS and the
-// outputs go out, four columns a thread.
-template <int WEIGHT, int G, int MF, int NF, bool GATED, bool OUT_FP8, int WN, int WK>
-__device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, float* part) {
-  constexpr bool ALONE = WK == 0;
-  constexpr int PARTS = ALONE ? 1 : WK;
+// The long list's form: the four wavefronts of a workgroup take strips beside
+// each other over all of k and share the rows of A through LDS. W still goes
+// straight into registers, D steps ahead; a step's A goes through registers,
+// also D steps ahead (a wait for a load waits for every older one too, so
+// both have to be ordered alike), and is written to LDS as the products read
+// it: as bf16, for int4 in the order of the codes.
+template <int WEIGHT>
+constexpr int step_columns = WEIGHT == kWeightBf16 ? 64 : 128;
+
+template <int WEIGHT, int G, int MF, int NF, bool GATED>
+__device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, const Item& mine,
+                                           uint8_t* abuf, f32x4 (&acc)[MF][NF]) {
+  constexpr bool FP8 = WEIGHT == kWeightFp8, INT4 = WEIGHT == kWeightInt4;
+  constexpr int KS = step_columns<WEIGHT>;
+  constexpr int ROW = 2 * KS;                       // LDS bytes of a row of a step
+  constexpr int STEP = MF * 16 * ROW;
+  constexpr int CH = ROW / 16;                      // 16-byte chunks of it
+  constexpr int D = MF == 4 ? 2 : 3;
+  constexpr int A_ITEM = FP8 ? 1 : 2;               // bytes of a value of A in memory
+  constexpr int A_CH = KS * A_ITEM / 16;            // 16-byte loads of a row
+  constexpr int AL = (MF * 16 * A_CH + 255) / 256;  // loads of a thread
+  constexpr int WL = KS * (FP8 ? 2 : INT4 ? 1 : 4) / 128;  // 16-byte loads of a strip
+  constexpr int GROUPS = INT4 ? 128 / G : 1;
+  const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
+  const int steps = (P.k + KS - 1) / KS;
+  const uint32_t lda = (uint32_t)P.k * A_ITEM;
+  const uint32_t ldw = INT4 ? (uint32_t)P.k / 2 : lda;
+  const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * lda);
+  const int rows_w = (GATED ? 2 : 1) * P.n;
+  Rsrc rw[NF];
+#pragma unroll
+  for (int f = 0; f < NF; ++f)
+    rw[f] = rsrc_of(P.w + ((uint64_t)it.e * rows_w + strip_row<NF, GATED>(P, mine.strip, f)) * ldw,
+                    (uint32_t)strip_rows<NF, GATED>(P, mine, f) * ldw);
+
+  // Scales. int4: lane quarter q loads strip q's and its zero points; fp8:
+  // quarter q loads row fragment q's and strip q's. Behind k: zeros.
+  const int groups = INT4 ? P.k / G : steps, blocks = (rows_w + 127) / 128;
+  const uint32_t values = (uint32_t)(FP8 ? blocks : rows_w) * groups;
+  const Rsrc rs = FP8 ? rsrc_of(static_cast<const float*>(P.w_scales) + (uint64_t)it.e * values, 4 * values)
+                      : rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)it.e * values, 2 * values);
+  const Rsrc rz = rsrc_of(P.w_zeros + (P.w_zeros ? (uint64_t)it.e * values : 0), P.w_zeros ? values : 0u);
+  const Rsrc ras = rsrc_of(it.a_scales, (uint32_t)it.rows * groups * 4u);
+  const float z_none = P.w_zeros ? 16.0f : 24.0f;
+  const int srow = strip_row<NF, GATED>(P, mine.strip, hi % NF);
+  const uint32_t s_at = FP8 ? 4u * (srow / 128) * groups : (uint32_t)(srow + lo) * groups;
+  const uint32_t as_at = 4u * ((MF > 1 ? hi % MF : 0) * 16 + lo) * groups;
+
+  v4u wb[D][NF][WL], ab[D][AL];
+  float as[D], sw[D];
+  uint32_t sb[D][GROUPS], zb[D][GROUPS];
+  auto load_a = [&](int s, int step) {
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int q = tid + 256 * i, row = q / A_CH;
+      const uint32_t at = (uint32_t)step * (KS * A_ITEM) + 16u * (q % A_CH);
+      const bool in = step < steps && at < lda && row < MF * 16;
+      ab[s][i] = load16(ra, in ? (uint32_t)row * lda + at : kOutside);
+    }
+  };
+  auto store_a = [&](int s, int step) {
+    uint8_t* to = abuf + (step & 1) * STEP;
+#pragma unroll
+    for (int i = 0; i < AL; ++i) {
+      const int q = tid + 256 * i, row = q / A_CH, c = q % A_CH;
+      if (MF * 16 * A_CH % 256 && row >= MF * 16) break;
+      uint8_t* r = to + row * ROW;
+      if constexpr (FP8) {
+        const Bf16x16 v = fp8_to_bf16(ab[s][i]);
+        *reinterpret_cast<bf16x8*>(r + (((2 * c) ^ row) & (CH - 1)) * 16) = v.lo;
+        *reinterpret_cast<bf16x8*>(r + (((2 * c + 1) ^ row) & (CH - 1)) * 16) = v.hi;
+      } else if constexpr (INT4) {
+        *reinterpret_cast<bf16x8*>(r + ((c ^ row) & (CH - 1)) * 16) = a_like_codes(ab[s][i]);
+      } else {
+        *reinterpret_cast<v4u*>(r + ((c ^ row) & (CH - 1)) * 16) = ab[s][i];
+      }
+    }
+  };
+  auto load_w = [&](int s, int step) {
+#pragma unroll
+    for (int j = 0; j < WL; ++j) {
+      const uint32_t at = (uint32_t)step * (64 * WL) + 64u * j + 16u * hi;
+      const uint32_t off = step < steps && at < ldw ? lo * ldw + at : kOutside;
+#pragma unroll
+      for (int f = 0; f < NF; ++f) wb[s][f][j] = load16(rw[f], off);
+    }
+    if constexpr (FP8) {
+      as[s] = load_f32(ras, step < steps ? as_at + 4u * step : kOutside);
+      sw[s] = load_f32(rs, step < steps ? s_at + 4u * step : kOutside);
+    }
+    if constexpr (INT4) {
+#pragma unroll
+      for (int u = 0; u < GROUPS; ++u) {
+        const int g = step * GROUPS + u;
+        const uint32_t at = s_at + (uint32_t)g;
+        sb[s][u] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(g < groups ? 2 * at : kOutside), 0, 0);
+        zb[s][u] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)(g < groups ? at : kOutside), 0, 0);
+      }
+    }
+  };
+  const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
+  const CodeMasks masks;
+  const f32x4 zero = {0, 0, 0, 0};
+  auto multiply = [&](int s, int step) __attribute__((always_inline)) {
+    const uint8_t* from = abuf + (step & 1) * STEP;
+    auto a_chunk = [&](int m, int c) {
+      const int row = m * 16 + lo;
+      return *reinterpret_cast<const bf16x8*>(from + row * ROW + ((c ^ row) & (CH - 1)) * 16);
+    };
+    if constexpr (WEIGHT == kWeightBf16) {
+#pragma unroll
+      for (int j = 0; j < WL; ++j)
+#pragma unroll
+        for (int m = 0; m < MF; ++m) {
+          const bf16x8 a = a_chunk(m, 4 * j + hi);
+#pragma unroll
+          for (int f = 0; f < NF; ++f)
+            acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                a, __builtin_bit_cast(bf16x8, wb[s][f][j]), acc[m][f], 0, 0, 0);
+        }
+    } else if constexpr (FP8) {
+      float av[MF];
+#pragma unroll
+      for (int m = 0; m < MF; ++m) av[m] = MF > 1 ? __shfl(as[s], m * 16 + lo, 64) : as[s];
+      constexpr int FB = MF == 4 ? 1 : NF;  // strips at a time
+#pragma unroll
+      for (int f0 = 0; f0 < NF; f0 += FB) {
+        f32x4 p[MF][FB];
+#pragma unroll
+        for (int j = 0; j < WL; ++j) {
+          Bf16x16 w[FB];
+#pragma unroll
+          for (int f = 0; f < FB; ++f) w[f] = fp8_to_bf16(wb[s][f0 + f][j]);
+#pragma unroll
+          for (int m = 0; m < MF; ++m) {
+            const bf16x8 a0 = a_chunk(m, 8 * j + 2 * hi), a1 = a_chunk(m, 8 * j + 2 * hi + 1);
+#pragma unroll
+            for (int f = 0; f < FB; ++f) {
+              p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f].lo, a0, j ? p[m][f] : zero, 0, 0, 0);
+              p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[f].hi, a1, p[m][f], 0, 0, 0);
+            }
+          }
+        }
+#pragma unroll
+        for (int f = 0; f < FB; ++f) {
+          const float wv = __builtin_bit_cast(
+              float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw[s]), (f0 + f) * 16));
+#pragma unroll
+          for (int m = 0; m < MF; ++m) {
+            const float sc = av[m] * wv;
+#pragma unroll
+            for (int r = 0; r < 4; ++r)
+              acc[m][f0 + f][r] = __builtin_fmaf(sc, p[m][f][r], acc[m][f0 + f][r]);
+          }
+        }
+        if (FB < NF) __builtin_amdgcn_sched_barrier(0);  // strips in turn, for the registers
+      }
+    } else {
+      // Groups of 128: the word j of quarter q holds columns 32 q + 8 j and on,
+      // and A is read to match. Smaller groups: transposed, see sum_int4.
+      uint32_t wt[NF][4];
+#pragma unroll
+      for (int f = 0; f < NF; ++f) {
+        wt[f][0] = wb[s][f][0].x, wt[f][1] = wb[s][f][0].y, wt[f][2] = wb[s][f][0].z, wt[f][3] = wb[s][f][0].w;
+        if constexpr (G < 128) transpose_quarters(wt[f]);
+      }
+#pragma unroll
+      for (int u = 0; u < GROUPS; ++u) {
+        const float scale = __uint_as_float(sb[s][u] << 16);
+        const float zero_at = z_none + (float)zb[s][u];
+        constexpr int FB = MF == 4 ? 1 : NF;
+        f32x4 sum[MF];
+#pragma unroll
+        for (int f0 = 0; f0 < NF; f0 += FB) {
+          f32x4 p[MF][FB];
+#pragma unroll
+          for (int j = u * (G / 32); j < (u + 1) * (G / 32); ++j) {
+            const bool start = j == u * (G / 32);
+            bf16x8 w[FB];
+#pragma unroll
+            for (int f = 0; f < FB; ++f) w[f] = codes_bf16(wt[f0 + f][j], masks);
+#pragma unroll
+            for (int m = 0; m < MF; ++m) {
+              const bf16x8 a = a_chunk(m, G < 128 ? 4 * j + hi : 4 * hi + j);
+              if (f0 == 0)
+                sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, start ? zero : sum[m], 0, 0, 0);
+#pragma unroll
+              for (int f = 0; f < FB; ++f)
+                p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w[f], start ? zero : p[m][f], 0, 0, 0);
+            }
+          }
+#pragma unroll
+          for (int f = 0; f < FB; ++f) {
+            const float sc = __shfl(scale, (f0 + f) * 16 + lo, 64);
+            const float off = __shfl(zero_at, (f0 + f) * 16 + lo, 64);
+#pragma unroll
+            for (int m = 0; m < MF; ++m)
+#pragma unroll
+              for (int r = 0; r < 4; ++r)
+                acc[m][f0 + f][r] = __builtin_fmaf(
+                    sc, __builtin_fmaf(-off, sum[m][r], p[m][f][r]), acc[m][f0 + f][r]);
+          }
+          if (FB < NF) __builtin_amdgcn_sched_barrier(0);  // strips in turn, for the registers
+        }
+        __builtin_amdgcn_sched_barrier(0);  // groups in turn: their registers do not add up
+      }
+    }
+  };
+
+  // ab[i] holds step i's rows of A (mod D), wb[i] its weights
+#pragma unroll
+  for (int s = 0; s < D; ++s) {
+    load_a(s, s);
+    load_w(s, s);
+  }
+  __syncthreads();  // the buffers' last reader is done
+  store_a(0, 0);
+  load_a(0, D);
+  for (int k = 0; k < steps; k += D) {
+#pragma unroll
+    for (int s = 0; s < D; ++s) {
+      const int step = k + s;
+      if (step >= steps) break;  // the same for the whole workgroup
+      __syncthreads();           // step's A is there, and the step before is read
+      store_a((s + 1) % D, step + 1);
+      load_a((s + 1) % D, step + 1 + D);
+      multiply(s, step);
+      load_w(s, step + D);
+    }
+  }
+}
+
+// One item. SPLIT: the wavefronts split k between them; else they take its
+// strips beside each other. Sums first, then, 16 rows at a time, they pass
+// through LDS and the outputs go out, four columns a thread.
+template <int WEIGHT, int G, int MF, int NF, bool GATED, bool OUT_FP8, bool SPLIT>
+__device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, float* part,
+                                        uint8_t* abuf) {
+  constexpr bool ALONE = !SPLIT && !OUT_FP8;
+  constexpr int WN = OUT_FP8 ? kFewWaves : 1;
+  constexpr int PARTS = SPLIT ? kFewWaves : 1;
   constexpr int SF = GATED ? NF / 2 : NF;   // output strips a wavefront
   constexpr int LD = NF * 16 + 4;           // floats of a partial row
   constexpr int COLS = WN * SF * 16;
-  constexpr int THREADS = ALONE ? 64 : WN * WK * 64;
+  constexpr int THREADS = ALONE ? 64 : kFewWaves * 64;
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tid = ALONE ? lane : threadIdx.x;
-  const int wn = ALONE ? 0 : wave % WN, kw = ALONE ? 0 : wave / WN;
   Item mine = it;
-  mine.strip = it.strip + wn * SF;
-  mine.strips = it.strips - wn * SF;
+  if constexpr (!SPLIT) {
+    const int s0 = it.strips * wave / kFewWaves;
+    mine.strip = it.strip + s0;
+    mine.strips = it.strips * (wave + 1) / kFewWaves - s0;
+  }
   f32x4 acc[MF][NF];
 #pragma unroll
   for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-  if constexpr (WEIGHT == kWeightBf16)
-    sum_bf16<MF, NF, GATED>(P, mine, kw, PARTS, acc);
+  if constexpr (!SPLIT)
+    sum_shared<WEIGHT, G, MF, NF, GATED>(P, it, mine, abuf, acc);
+  else if constexpr (WEIGHT == kWeightBf16)
+    sum_bf16<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
   else if constexpr (WEIGHT == kWeightFp8)
-    sum_fp8<MF, NF, GATED>(P, mine, kw, PARTS, acc);
+    sum_fp8<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
   else
-    sum_int4<MF, NF, GATED, G>(P, mine, kw, PARTS, acc);
+    sum_int4<MF, NF, GATED, G>(P, mine, wave, kFewWaves, acc);
 
   auto meet = [] {
     if constexpr (ALONE) {
@@ -372,7 +652,7 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
       f32x4 v = {0, 0, 0, 0}, u = {0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
-        const float* p = first + (q * WN + list) * 16 * kPartLd + row * LD + at;
+        const float* p = first + (SPLIT ? q : list) * 16 * kPartLd + row * LD + at;
         v += *reinterpret_cast<const f32x4*>(p);
         if constexpr (GATED) u += *reinterpret_cast<const f32x4*>(p + SF * 16);
       }
@@ -380,8 +660,9 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
 #pragma unroll
         for (int r = 0; r < 4; ++r) v[r] = silu_mul(v[r], u[r]);
       }
-      const int col = it.strip * 16 + c4;
-      const bool in = m * 16 + row < it.rows && col < P.n && c4 < it.strips * 16;
+      const Item& of = ALONE ? mine : it;
+      const int col = of.strip * 16 + c4;
+      const bool in = m * 16 + row < it.rows && col < P.n && c4 < of.strips * 16;
       const uint64_t orow = (uint64_t)(it.row0 + m * 16 + row);
       if constexpr (OUT_FP8) {
         // 32 lanes hold a row's 128 columns
@@ -405,31 +686,32 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
   }
 }
 
-template <int WEIGHT, int G, int NF, bool GATED, bool OUT_FP8, int WN, int WK>
-__device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it, float* part) {
+template <int WEIGHT, int G, int NF, bool GATED, bool OUT_FP8, bool SPLIT>
+__device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it, float* part,
+                                             uint8_t* abuf) {
   if (it.rows <= 16) {
-    do_item<WEIGHT, G, 1, NF, GATED, OUT_FP8, WN, WK>(P, it, part);
+    do_item<WEIGHT, G, 1, NF, GATED, OUT_FP8, SPLIT>(P, it, part, abuf);
   } else if (it.rows <= 32) {
-    do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, WN, WK>(P, it, part);
-  } else if constexpr (WEIGHT == kWeightInt4 && NF == 4) {
+    do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, it, part, abuf);
+  } else if constexpr (SPLIT && WEIGHT != kWeightBf16 && NF == 4) {
     // registers hold 64 rows of A beside two strips
     constexpr int SF = GATED ? 1 : 2;
     Item half = it;
     half.strips = it.strips < SF ? it.strips : SF;
-    do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, WN, WK>(P, half, part);
+    do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, part, abuf);
     half.strip += SF;
     half.strips = it.strips - SF;
-    if (half.strips > 0) do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, WN, WK>(P, half, part);
+    if (half.strips > 0) do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, part, abuf);
   } else {
-    do_item<WEIGHT, G, 4, NF, GATED, OUT_FP8, WN, WK>(P, it, part);
+    do_item<WEIGHT, G, 4, NF, GATED, OUT_FP8, SPLIT>(P, it, part, abuf);
   }
 }
 
 // The units [u0, u1) of a list of `tiles` x `units`. A unit is an output
 // strip, or (fp8 out, where a row's 128 columns share a scale) 128 columns.
-template <int WEIGHT, int G, bool GATED, bool OUT_FP8, int WN, int WK>
-__device__ __forceinline__ void do_run(const GemmParams& P, const uint32_t* pre, float* part, int units,
-                                       uint64_t u0, uint64_t u1) {
+template <int WEIGHT, int G, bool GATED, bool OUT_FP8, bool SPLIT>
+__device__ __forceinline__ void do_run(const GemmParams& P, const uint32_t* pre, float* part,
+                                       uint8_t* abuf, int units, uint64_t u0, uint64_t u1) {
   constexpr int SF = GATED ? kFewFrags / 2 : kFewFrags;
   if (u0 >= u1) return;
   // division in 32 bits wherever the list allows it
@@ -456,61 +738,58 @@ __device__ __forceinline__ void do_run(const GemmParams& P, const uint32_t* pre,
     int here = units - unit;
     here = left < (uint64_t)here ? (int)left : here;
     int done = 1;
+    it.strip = unit;
     if constexpr (OUT_FP8) {
-      static_assert(WN * SF == 8, "a workgroup holds 128 columns");
       it.strip = unit * 8;
       it.strips = 8;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, WN, WK>(P, it, part);
+      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, part, abuf);
+    } else if constexpr (!SPLIT) {
+      // as many strips as the workgroup holds, in items of like size
+      const int items = (here + kFewWaves * SF - 1) / (kFewWaves * SF);
+      it.strips = done = (here + items - 1) / items;
+      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, part, abuf);
     } else if (here >= SF) {
-      it.strip = unit;
       it.strips = done = SF;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, WN, WK>(P, it, part);
+      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, true>(P, it, part, abuf);
     } else {
       // the run's last strips, fewer than a wavefront holds
-      it.strip = unit;
       it.strips = 1;
-      do_item_rows<WEIGHT, G, GATED ? 2 : 1, GATED, OUT_FP8, WN, WK>(P, it, part);
+      do_item_rows<WEIGHT, G, GATED ? 2 : 1, GATED, OUT_FP8, true>(P, it, part, abuf);
     }
     unit += done;
     left -= done;
   }
 }
 
-// Workgroups: two a CU (one of twice the size for the fp8 output). A power of
-// two, so that the runs need no division.
-constexpr int few_blocks_log2(bool out_fp8) { return out_fp8 ? 8 : 9; }
+// Workgroups: two a CU. A power of two, so that the runs need no division.
+constexpr int kFewBlocksLog2 = 9;
 
-template <int WEIGHT, int G, bool GATED, bool OUT_FP8, int WN, int WK>
-__global__ void __launch_bounds__(WN* WK * 64, 2) gemm_few_kernel(const GemmParams P, int most) {
+template <int WEIGHT, int G, bool GATED, bool OUT_FP8>
+__global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmParams P, int most) {
   extern __shared__ __align__(16) uint8_t lds_raw[];
-  __shared__ uint32_t scan[WN * WK];
-  __shared__ __align__(16) float part[WN * WK * 16 * kPartLd];
+  __shared__ uint32_t scan[kFewWaves];
+  __shared__ __align__(16) float part[kFewWaves * 16 * kPartLd];
+  __shared__ __align__(16) uint8_t abuf[2 * kFewRows * 2 * step_columns<WEIGHT>];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
-  tile_prefix<WN * WK * 64>(P, kFewRows, 0, most, pre, scan);
+  tile_prefix<kFewWaves * 64>(P, kFewRows, 0, most, pre, scan);
   const uint32_t tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
   const int units = OUT_FP8 ? P.n / 128 : (P.n + 15) / 16;
   const uint64_t total = (uint64_t)tiles * units;
-  constexpr int LOG = few_blocks_log2(OUT_FP8);
-  if constexpr (!OUT_FP8) {
-    // Alone a wavefront needs some strips to be busy with.
-    constexpr int LOG1 = LOG + 2;
-    static_assert(WN * WK == 4, "wavefronts of a workgroup");
-    if (total >> LOG1 >= 2 * (GATED ? kFewFrags / 2 : kFewFrags)) {
-      const uint32_t w = blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-      do_run<WEIGHT, G, GATED, OUT_FP8, 1, 0>(P, pre, part, units, total * w >> LOG1,
-                                              total * (w + 1) >> LOG1);
-      return;
-    }
-  }
-  do_run<WEIGHT, G, GATED, OUT_FP8, WN, WK>(P, pre, part, units, total * blockIdx.x >> LOG,
-                                            total * (blockIdx.x + 1) >> LOG);
+  // Workgroups are dealt to the XCDs in turn; neighbours in the list, which
+  // share rows of A, go to one XCD and its L2.
+  constexpr int LOG = kFewBlocksLog2;
+  const uint32_t at = (blockIdx.x % kXcds << LOG) / kXcds + blockIdx.x / kXcds;
+  const uint64_t u0 = total * at >> LOG, u1 = total * (at + 1) >> LOG;
+  if (OUT_FP8 || total >> LOG >= kFewLong * (GATED ? kFewFrags / 2 : kFewFrags))
+    do_run<WEIGHT, G, GATED, OUT_FP8, false>(P, pre, part, abuf, units, u0, u1);
+  else
+    do_run<WEIGHT, G, GATED, OUT_FP8, true>(P, pre, part, abuf, units, u0, u1);
 }
 
 template <int WEIGHT, int G, bool GATED, bool OUT_FP8>
 hipError_t launch(const GemmParams& p, int most, hipStream_t stream) {
-  constexpr int WN = OUT_FP8 ? 4 : 1, WK = OUT_FP8 ? 2 : 4;
-  gemm_few_kernel<WEIGHT, G, GATED, OUT_FP8, WN, WK>
-      <<<1 << few_blocks_log2(OUT_FP8), WN * WK * 64, tile_prefix_bytes(p.num_experts), stream>>>(p, most);
+  gemm_few_kernel<WEIGHT, G, GATED, OUT_FP8>
+      <<<1 << kFewBlocksLog2, kFewWaves * 64, tile_prefix_bytes(p.num_experts), stream>>>(p, most);
   return hipGetLastError();
 }
 

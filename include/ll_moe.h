@@ -407,7 +407,7 @@ int ll_moe_expert_gemm(int max_tokens, int n, int k, int num_experts, int dtype,
  *   w_scales: device bf16 [num_experts, n or 2n, k / group].
  *   w_zeros:  device uint8 [num_experts, n or 2n, k / group], or NULL: 8.
  *   out:      bf16.
- * No weight is rounded: a group's codes are multiplied and summed in fp32 and
+ * An expert has fewer than 2^30 scales. No weight is rounded: a group's codes are multiplied and summed in fp32 and
  * the scale is applied to the sum. The sum is taken as sum((16 + code) * A) -
  * (16 + z) * sum(A): a row that holds an infinity (or magnitudes whose 31-fold
  * sums leave fp32's range) gives NaN. Everything else as ll_moe_expert_gemm.
