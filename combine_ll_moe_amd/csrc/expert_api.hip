@@ -113,7 +113,7 @@ extern "C" int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_exper
   if (k % group || n % 8) return LL_MOE_INVALID_ARGUMENT;
   if (!a || !w || !w_scales || !counts || !out) return LL_MOE_INVALID_ARGUMENT;
   if (!aligned(a, 16) || !aligned(w, 16) || !aligned(out, 16) || !aligned(counts, 4) ||
-      !aligned(w_scales, 2))
+      !aligned(w_scales, 16) || !aligned(w_zeros, 8))
     return LL_MOE_INVALID_ARGUMENT;
   const bool gated = act == LL_MOE_ACT_SILU_MUL;
   const uint64_t rows = (uint64_t)num_experts * max_tokens, rows_w = gated ? 2 * (uint64_t)n : n;

@@ -42,6 +42,8 @@ constexpr int kFewWaves = 4;      // of a workgroup
 // the list is long.
 constexpr int kFewLong = 4;
 constexpr int kPartLd = kFewFrags * 16 + 4;  // floats of a row of partial sums, at most
+constexpr int kPartFloats = 1152;            // a wavefront's 16 rows of them, or its ring of scales
+static_assert(kPartFloats >= 16 * kPartLd);
 
 __device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
@@ -249,18 +251,95 @@ __device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
   swap16(w[2], w[3]);
 }
 
+// A wavefront's int4 scales and zero points. A group's value of 64 weight rows
+// lies in 64 cache lines, so loads a group at a time would ask the caches for
+// as much as the codes do; here a lane takes the next 16 bytes (8 groups) of
+// one row's scales and 8 of its zero points, whole aligned blocks, into a
+// ring of two blocks a row in LDS, and every lane reads its rows' values from
+// there. A row starts anywhere in a block: a window of 8 groups touches two.
+template <int NF, bool GATED>
+struct ScaleRing {
+  static constexpr int kRow = 48, kZeroRow = 24;  // LDS bytes of a row, spread over the banks
+  static constexpr int kBytes = 64 * (kRow + kZeroRow);
+  Rsrc rs, rz;
+  uint8_t* lds;
+  uint32_t block, zblock;       // this lane's next block's offset
+  v4u next;
+  v2u znext;
+  uint32_t at[NF], zat[NF];     // LDS: row f * 16 + lane % 16
+  uint32_t phase[NF], zphase[NF];
+  float none;
+  static_assert(kBytes <= 4 * kPartFloats);
+
+  __device__ __forceinline__ void init(const GemmParams& P, const Item& it, int groups, int first,
+                                       uint8_t* ring) {
+    const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
+    const int rows_w = (GATED ? 2 : 1) * P.n;
+    const uint32_t values = (uint32_t)rows_w * groups;
+    rs = rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)it.e * values, 2 * values);
+    // without zero points their descriptor is empty
+    rz = rsrc_of(P.w_zeros + (P.w_zeros ? (uint64_t)it.e * values : 0), P.w_zeros ? values : 0u);
+    none = P.w_zeros ? 16.0f : 24.0f;
+    lds = ring;
+    const uint32_t g0 = (uint32_t)(strip_row<NF, GATED>(P, it.strip, hi % NF) + lo) * groups + first;
+    block = 2 * g0 & ~15u;
+    zblock = g0 & ~7u;
+#pragma unroll
+    for (int f = 0; f < NF; ++f) {
+      const uint32_t g = (uint32_t)(strip_row<NF, GATED>(P, it.strip, f) + lo) * groups + first;
+      at[f] = (f * 16 + lo) * kRow;
+      zat[f] = 64 * kRow + (f * 16 + lo) * kZeroRow;
+      phase[f] = 2 * g & 15;
+      zphase[f] = g & 7;
+    }
+    fetch();
+    put(0);
+    fetch();
+    put(1);
+    fetch();
+  }
+  __device__ __forceinline__ void fetch() {
+    next = load16(rs, block);
+    znext = __builtin_amdgcn_raw_buffer_load_b64(rz, (int)zblock, 0, 0);
+    block += 16;
+    zblock += 8;
+  }
+  __device__ __forceinline__ void put(int slot) {
+    const int lane = threadIdx.x & 63;
+    *reinterpret_cast<v4u*>(lds + lane * kRow + slot * 16) = next;
+    *reinterpret_cast<v2u*>(lds + 64 * kRow + lane * kZeroRow + slot * 8) = znext;
+  }
+  // Before group g (from `first`) is read: at a window's start the block
+  // behind it comes in, in the place of the one before it.
+  __device__ __forceinline__ void enter(int g) {
+    if (g > 0 && g % 8 == 0) {
+      put((g / 8 + 1) & 1);
+      fetch();
+    }
+  }
+  __device__ __forceinline__ float scale(int f, int g) const {
+    return __uint_as_float(
+        (uint32_t) * reinterpret_cast<const uint16_t*>(lds + at[f] + ((phase[f] + 2 * g) & 31)) << 16);
+  }
+  __device__ __forceinline__ float zero(int f, int g) const {
+    return none + (float)lds[zat[f] + ((zphase[f] + g) & 15)];
+  }
+};
+
 // A chunk is 128 columns: 16 bytes of codes a lane, quarter q the columns
 // [32 q, 32 q + 32). Transposed among the quarters, word j of quarter q holds
 // columns 32 j + 8 q and on: product j covers columns [32 j, 32 j + 32), which
 // lie in one group, and A's fragments are read as they stand.
 template <int MF, int NF, bool GATED, int G>
 __device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, int kw, int WK,
-                                         f32x4 (&acc)[MF][NF]) {
+                                         uint8_t* ring_lds, f32x4 (&acc)[MF][NF]) {
   constexpr int D = MF == 4 ? 1 : MF == 2 ? 2 : 3;
   constexpr int GROUPS = 128 / G;  // of a chunk
   const int lane = threadIdx.x & 63;
   const uint32_t lda = 2u * (uint32_t)P.k, ldw = (uint32_t)P.k / 2;
   const int groups = P.k / G, chunks = (P.k + 127) / 128;
+  // a run of chunks for each wavefront, for its ring of scales
+  const int c0 = chunks * kw / WK, c1 = chunks * (kw + 1) / WK;
   const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * lda);
   Rsrc rw[NF];
   const int rows_w = (GATED ? 2 : 1) * P.n;
@@ -269,44 +348,32 @@ __device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, in
     rw[f] = rsrc_of(P.w + ((uint64_t)it.e * rows_w + strip_row<NF, GATED>(P, it.strip, f)) * ldw,
                     (uint32_t)strip_rows<NF, GATED>(P, it, f) * ldw);
   const uint32_t lo = lane & 15, hi = lane >> 4;
-  // Lane quarter q loads strip q's scales and zero points; those of a group
-  // behind k are zeros. Without zero points their descriptor is empty.
-  const uint32_t values = (uint32_t)rows_w * groups;
-  const Rsrc rs = rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)it.e * values, 2 * values);
-  const Rsrc rz = rsrc_of(P.w_zeros + (P.w_zeros ? (uint64_t)it.e * values : 0), P.w_zeros ? values : 0u);
-  const float z_none = P.w_zeros ? 16.0f : 24.0f;
-  const uint32_t s_at = (uint32_t)(strip_row<NF, GATED>(P, it.strip, (int)hi % NF) + (int)lo) * groups;
+  ScaleRing<NF, GATED> ring;
   v4u wb[D][NF], ab[D][MF][4];
-  uint32_t sb[D][GROUPS], zb[D][GROUPS];
   auto load = [&](int s, int c) {
     const uint32_t wat = 64u * (uint32_t)c + 16u * hi;
-    const uint32_t woff = c < chunks && wat < ldw ? lo * ldw + wat : kOutside;
+    const uint32_t woff = c < c1 && wat < ldw ? lo * ldw + wat : kOutside;
 #pragma unroll
     for (int f = 0; f < NF; ++f) wb[s][f] = load16(rw[f], woff);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const uint32_t at = 256u * (uint32_t)c + 64u * j + 16u * hi;
-      const bool in = c < chunks && at < lda;
+      const bool in = c < c1 && at < lda;
 #pragma unroll
       for (int m = 0; m < MF; ++m)
         ab[s][m][j] = load16(ra, in ? (lo + m * 16u) * lda + at : kOutside);
-    }
-#pragma unroll
-    for (int u = 0; u < GROUPS; ++u) {
-      const int g = c * GROUPS + u;
-      const uint32_t at = s_at + (uint32_t)g;
-      sb[s][u] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(g < groups ? 2 * at : kOutside), 0, 0);
-      zb[s][u] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)(g < groups ? at : kOutside), 0, 0);
     }
   };
   const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
   const CodeMasks masks;
 #pragma unroll
-  for (int s = 0; s < D; ++s) load(s, kw + s * WK);
-  for (int c = kw; c < chunks; c += D * WK) {
+  for (int s = 0; s < D; ++s) load(s, c0 + s);
+  ring.init(P, it, groups, c0 * GROUPS, ring_lds);
+  for (int c = c0; c < c1; c += D) {
 #pragma unroll
     for (int s = 0; s < D; ++s) {
+      if (c + s >= c1) break;
       const f32x4 zero = {0, 0, 0, 0};
       uint32_t wt[NF][4];
 #pragma unroll
@@ -314,10 +381,10 @@ __device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, in
         wt[f][0] = wb[s][f].x, wt[f][1] = wb[s][f].y, wt[f][2] = wb[s][f].z, wt[f][3] = wb[s][f].w;
         transpose_quarters(wt[f]);
       }
+      ring.enter((c + s - c0) * GROUPS);
 #pragma unroll
       for (int u = 0; u < GROUPS; ++u) {
-        const float scale = __uint_as_float(sb[s][u] << 16);
-        const float zero_at = z_none + (float)zb[s][u];
+        const int g = (c + s) * GROUPS + u;
         f32x4 p[MF][NF], sum[MF];
 #pragma unroll
         for (int j = u * (G / 32); j < (u + 1) * (G / 32); ++j) {
@@ -338,8 +405,10 @@ __device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, in
         }
 #pragma unroll
         for (int f = 0; f < NF; ++f) {
-          const float sc = __shfl(scale, f * 16 + (int)lo, 64);
-          const float off = __shfl(zero_at, f * 16 + (int)lo, 64);
+          // a group behind k is zeros, times what may be a NaN: scale 0
+          const float read = ring.scale(f, g - c0 * GROUPS);
+          const float sc = g < groups ? read : 0.0f;
+          const float off = ring.zero(f, g - c0 * GROUPS);
 #pragma unroll
           for (int m = 0; m < MF; ++m)
 #pragma unroll
@@ -348,7 +417,7 @@ __device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, in
         }
         __builtin_amdgcn_sched_barrier(0);  // groups in turn: their registers do not add up
       }
-      load(s, c + (s + D) * WK);
+      load(s, c + s + D);
     }
   }
 }
@@ -364,7 +433,8 @@ constexpr int step_columns = WEIGHT == kWeightBf16 ? 64 : 128;
 
 template <int WEIGHT, int G, int MF, int NF, bool GATED>
 __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, const Item& mine,
-                                           uint8_t* abuf, f32x4 (&acc)[MF][NF]) {
+                                           uint8_t* abuf, uint8_t* ring_lds,
+                                           f32x4 (&acc)[MF][NF]) {
   constexpr bool FP8 = WEIGHT == kWeightFp8, INT4 = WEIGHT == kWeightInt4;
   constexpr int KS = step_columns<WEIGHT>;
   constexpr int ROW = 2 * KS;                       // LDS bytes of a row of a step
@@ -388,22 +458,18 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
     rw[f] = rsrc_of(P.w + ((uint64_t)it.e * rows_w + strip_row<NF, GATED>(P, mine.strip, f)) * ldw,
                     (uint32_t)strip_rows<NF, GATED>(P, mine, f) * ldw);
 
-  // Scales. int4: lane quarter q loads strip q's and its zero points; fp8:
-  // quarter q loads row fragment q's and strip q's. Behind k: zeros.
+  // Scales. fp8: lane quarter q loads row fragment q's and strip q's; those
+  // behind k are zeros. int4: a ring.
   const int groups = INT4 ? P.k / G : steps, blocks = (rows_w + 127) / 128;
-  const uint32_t values = (uint32_t)(FP8 ? blocks : rows_w) * groups;
-  const Rsrc rs = FP8 ? rsrc_of(static_cast<const float*>(P.w_scales) + (uint64_t)it.e * values, 4 * values)
-                      : rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)it.e * values, 2 * values);
-  const Rsrc rz = rsrc_of(P.w_zeros + (P.w_zeros ? (uint64_t)it.e * values : 0), P.w_zeros ? values : 0u);
-  const Rsrc ras = rsrc_of(it.a_scales, (uint32_t)it.rows * groups * 4u);
-  const float z_none = P.w_zeros ? 16.0f : 24.0f;
-  const int srow = strip_row<NF, GATED>(P, mine.strip, hi % NF);
-  const uint32_t s_at = FP8 ? 4u * (srow / 128) * groups : (uint32_t)(srow + lo) * groups;
+  const Rsrc rs = rsrc_of(static_cast<const float*>(P.w_scales) + (FP8 ? (uint64_t)it.e * blocks * groups : 0),
+                          FP8 ? 4u * blocks * groups : 0u);
+  const Rsrc ras = rsrc_of(it.a_scales, FP8 ? (uint32_t)it.rows * groups * 4u : 0u);
+  const uint32_t s_at = 4u * (strip_row<NF, GATED>(P, mine.strip, hi % NF) / 128) * groups;
   const uint32_t as_at = 4u * ((MF > 1 ? hi % MF : 0) * 16 + lo) * groups;
+  ScaleRing<NF, GATED> ring;
 
   v4u wb[D][NF][WL], ab[D][AL];
   float as[D], sw[D];
-  uint32_t sb[D][GROUPS], zb[D][GROUPS];
   auto load_a = [&](int s, int step) {
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
@@ -442,15 +508,6 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
     if constexpr (FP8) {
       as[s] = load_f32(ras, step < steps ? as_at + 4u * step : kOutside);
       sw[s] = load_f32(rs, step < steps ? s_at + 4u * step : kOutside);
-    }
-    if constexpr (INT4) {
-#pragma unroll
-      for (int u = 0; u < GROUPS; ++u) {
-        const int g = step * GROUPS + u;
-        const uint32_t at = s_at + (uint32_t)g;
-        sb[s][u] = __builtin_amdgcn_raw_buffer_load_b16(rs, (int)(g < groups ? 2 * at : kOutside), 0, 0);
-        zb[s][u] = __builtin_amdgcn_raw_buffer_load_b8(rz, (int)(g < groups ? at : kOutside), 0, 0);
-      }
     }
   };
   const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
@@ -514,6 +571,7 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
     } else {
       // Groups of 128: the word j of quarter q holds columns 32 q + 8 j and on,
       // and A is read to match. Smaller groups: transposed, see sum_int4.
+      ring.enter(step * GROUPS);
       uint32_t wt[NF][4];
 #pragma unroll
       for (int f = 0; f < NF; ++f) {
@@ -522,8 +580,7 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
       }
 #pragma unroll
       for (int u = 0; u < GROUPS; ++u) {
-        const float scale = __uint_as_float(sb[s][u] << 16);
-        const float zero_at = z_none + (float)zb[s][u];
+        const int g = step * GROUPS + u;
         constexpr int FB = MF == 4 ? 1 : NF;
         f32x4 sum[MF];
 #pragma unroll
@@ -547,8 +604,10 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
           }
 #pragma unroll
           for (int f = 0; f < FB; ++f) {
-            const float sc = __shfl(scale, (f0 + f) * 16 + lo, 64);
-            const float off = __shfl(zero_at, (f0 + f) * 16 + lo, 64);
+            // a group behind k is zeros, times what may be a NaN: scale 0
+            const float read = ring.scale(f0 + f, g);
+            const float sc = G == 128 || g < groups ? read : 0.0f;
+            const float off = ring.zero(f0 + f, g);
 #pragma unroll
             for (int m = 0; m < MF; ++m)
 #pragma unroll
@@ -569,6 +628,7 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
     load_a(s, s);
     load_w(s, s);
   }
+  if constexpr (INT4) ring.init(P, mine, groups, 0, ring_lds);
   __syncthreads();  // the buffers' last reader is done
   store_a(0, 0);
   load_a(0, D);
@@ -613,14 +673,16 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
   for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
+  // a wavefront's ring of scales and, after the sums, its part of them
+  uint8_t* ring = reinterpret_cast<uint8_t*>(part + wave * kPartFloats);
   if constexpr (!SPLIT)
-    sum_shared<WEIGHT, G, MF, NF, GATED>(P, it, mine, abuf, acc);
+    sum_shared<WEIGHT, G, MF, NF, GATED>(P, it, mine, abuf, ring, acc);
   else if constexpr (WEIGHT == kWeightBf16)
     sum_bf16<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
   else if constexpr (WEIGHT == kWeightFp8)
     sum_fp8<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
   else
-    sum_int4<MF, NF, GATED, G>(P, mine, wave, kFewWaves, acc);
+    sum_int4<MF, NF, GATED, G>(P, mine, wave, kFewWaves, ring, acc);
 
   auto meet = [] {
     if constexpr (ALONE) {
@@ -631,7 +693,7 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
     }
   };
   const int lo = lane & 15, hi = lane >> 4;
-  float* mp = part + wave * 16 * kPartLd;
+  float* mp = part + wave * kPartFloats;
   const float* first = ALONE ? mp : part;
 #pragma unroll
   for (int m = 0; m < MF; ++m) {
@@ -652,7 +714,7 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
       f32x4 v = {0, 0, 0, 0}, u = {0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
-        const float* p = first + (SPLIT ? q : list) * 16 * kPartLd + row * LD + at;
+        const float* p = first + (SPLIT ? q : list) * kPartFloats + row * LD + at;
         v += *reinterpret_cast<const f32x4*>(p);
         if constexpr (GATED) u += *reinterpret_cast<const f32x4*>(p + SF * 16);
       }
@@ -768,7 +830,7 @@ template <int WEIGHT, int G, bool GATED, bool OUT_FP8>
 __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmParams P, int most) {
   extern __shared__ __align__(16) uint8_t lds_raw[];
   __shared__ uint32_t scan[kFewWaves];
-  __shared__ __align__(16) float part[kFewWaves * 16 * kPartLd];
+  __shared__ __align__(16) float part[kFewWaves * kPartFloats];
   __shared__ __align__(16) uint8_t abuf[2 * kFewRows * 2 * step_columns<WEIGHT>];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
   tile_prefix<kFewWaves * 64>(P, kFewRows, 0, most, pre, scan);

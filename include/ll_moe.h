@@ -404,8 +404,9 @@ int ll_moe_expert_gemm(int max_tokens, int n, int k, int num_experts, int dtype,
  *   w:        device [num_experts, n or 2n, k / 2] bytes, 16-byte aligned: the
  *             code (0..15) of an even c in the low half of byte c / 2, of the
  *             odd c behind it in the high half.
- *   w_scales: device bf16 [num_experts, n or 2n, k / group].
- *   w_zeros:  device uint8 [num_experts, n or 2n, k / group], or NULL: 8.
+ *   w_scales: device bf16 [num_experts, n or 2n, k / group], 16-byte aligned.
+ *   w_zeros:  device uint8 [num_experts, n or 2n, k / group], 8-byte aligned,
+ *             or NULL: 8.
  *   out:      bf16.
  * An expert has fewer than 2^30 scales. No weight is rounded: a group's codes are multiplied and summed in fp32 and
  * the scale is applied to the sum. The sum is taken as sum((16 + code) * A) -

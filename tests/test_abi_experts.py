@@ -54,7 +54,7 @@ def test_fp8_gemm_refuses(case):
 
 @pytest.mark.parametrize("case", [
     dict(group=16), dict(group=0), dict(group=256), dict(k=544), dict(n=4), dict(act=3), dict(e=0), dict(a=0),
-    dict(w=0), dict(s=0), dict(counts=0), dict(out=0), dict(a=M + 2), dict(w=2 * M + 8), dict(s=3 * M + 1),
+    dict(w=0), dict(s=0), dict(counts=0), dict(out=0), dict(a=M + 2), dict(w=2 * M + 8), dict(s=3 * M + 8), dict(z=4 * M + 4),
     dict(counts=5 * M + 1), dict(out=6 * M + 4), dict(out=4 * M), dict(out=3 * M), dict(out=2 * M), dict(cap=1 << 29),
     dict(cap=1, e=1, n=1 << 20, k=1 << 15, group=32, out=1 << 50, w=1 << 51),
 ])
