@@ -107,23 +107,30 @@ def _ptr(a):
     return a.data_ptr()
 
 
-def _operand(call: str, a, device):
-    """Address of a contiguous tensor on `device` (or of a raw address): the
-    kernels take whole arrays, and run where the stream is."""
-    if a is None or isinstance(a, int):
-        return a
-    if not a.is_contiguous() or a.device != device:
-        raise LLMoEError(INVALID_ARGUMENT, call)
-    return a.data_ptr()
-
-
-def _operands(call: str, *tensors) -> list:
-    device = next((a.device for a in tensors if hasattr(a, "device")), None)
-    if device is not None:
-        import torch
-        if device.type != "cuda" or device.index != torch.cuda.current_device():
+def _operands(call: str, stream, *tensors) -> list:
+    """Addresses of contiguous tensors on the current device (or raw addresses
+    as they are), then the stream: the kernels take whole arrays and run where
+    the stream is. Torch's accessors of the device and the current stream make
+    Python objects, which takes longer than a small kernel; these return
+    numbers."""
+    out, device = [], None
+    for a in tensors:
+        if a is None or type(a) is int:
+            out.append(a)
+            continue
+        d = a.get_device()
+        if d < 0 or (device is not None and d != device) or not a.is_contiguous():
             raise LLMoEError(INVALID_ARGUMENT, call)
-    return [_operand(call, a, device) for a in tensors]
+        device = d
+        out.append(a.data_ptr())
+    if device is None:
+        out.append(_stream(stream))
+        return out
+    from torch import _C
+    if device != _C._cuda_getDevice():
+        raise LLMoEError(INVALID_ARGUMENT, call)
+    out.append(_C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
+    return out
 
 
 def _stream(s):
@@ -196,27 +203,30 @@ def ll_moe_expert_gemm(max_tokens: int, n: int, k: int, num_experts: int, dtype:
                        stream=None) -> None:
     """Products grouped by expert (bf16 or fp8), plain or gated. Tensors are
     contiguous and on the current device."""
-    ptrs = _operands("ll_moe_expert_gemm", a, a_scales, w, w_scales, counts, out, out_scales)
-    _check(_lib.ll_moe_expert_gemm(max_tokens, n, k, num_experts, dtype, act, out_dtype, *ptrs,
-                                   _stream(stream)), "ll_moe_expert_gemm")
+    _check(_lib.ll_moe_expert_gemm(max_tokens, n, k, num_experts, dtype, act, out_dtype,
+                                   *_operands("ll_moe_expert_gemm", stream, a, a_scales, w,
+                                              w_scales, counts, out, out_scales)),
+           "ll_moe_expert_gemm")
 
 
 def ll_moe_expert_gemm_w4(max_tokens: int, n: int, k: int, num_experts: int, group: int, act: int,
                           a, w, w_scales, w_zeros, counts, out, stream=None) -> None:
     """Products grouped by expert with 4-bit weights and a scale (and zero
     point) a group. Tensors are contiguous and on the current device."""
-    ptrs = _operands("ll_moe_expert_gemm_w4", a, w, w_scales, w_zeros, counts, out)
-    _check(_lib.ll_moe_expert_gemm_w4(max_tokens, n, k, num_experts, group, act, *ptrs,
-                                      _stream(stream)), "ll_moe_expert_gemm_w4")
+    _check(_lib.ll_moe_expert_gemm_w4(max_tokens, n, k, num_experts, group, act,
+                                      *_operands("ll_moe_expert_gemm_w4", stream, a, w, w_scales,
+                                                 w_zeros, counts, out)),
+           "ll_moe_expert_gemm_w4")
 
 
 def ll_moe_rms_norm(num_tokens: int, hidden: int, x_dtype: int, out_dtype: int, eps: float, x,
                     residual, weight, residual_out, out, out_scales=None, stream=None) -> None:
     """Root-mean-square norm of x plus the residual. Tensors are contiguous
     and on the current device."""
-    ptrs = _operands("ll_moe_rms_norm", x, residual, weight, residual_out, out, out_scales)
-    _check(_lib.ll_moe_rms_norm(num_tokens, hidden, x_dtype, out_dtype, eps, *ptrs,
-                                _stream(stream)), "ll_moe_rms_norm")
+    _check(_lib.ll_moe_rms_norm(num_tokens, hidden, x_dtype, out_dtype, eps,
+                                *_operands("ll_moe_rms_norm", stream, x, residual, weight,
+                                           residual_out, out, out_scales)),
+           "ll_moe_rms_norm")
 
 
 def ll_moe_clean_signals(layout, max_tokens: int, hidden: int, num_experts: int, dtype: int,

@@ -32,9 +32,11 @@ __device__ __forceinline__ v4u pack8(const float (&f)[8]) {
              bf16_pair(f[6], f[7])};
 }
 
+constexpr int kFewTokens = 256;
+
 // ROW: threads of a row; C: chunks of 8 columns a thread holds. A workgroup
 // of max(ROW, 256) threads takes rows side by side.
-template <int ROW, int C, bool X_FP32, bool OUT_FP8>
+template <int ROW, int C, bool X_FP32, bool RESIDUAL, bool OUT_FP8>
 __global__ void __launch_bounds__(ROW < 256 ? 256 : ROW) norm_kernel(const NormParams P) {
   constexpr int BLOCK = ROW < 256 ? 256 : ROW;
   __shared__ float part[BLOCK / 64];
@@ -44,38 +46,43 @@ __global__ void __launch_bounds__(ROW < 256 ? 256 : ROW) norm_kernel(const NormP
   const bool live = row < P.num_tokens;
   const int chunks = P.hidden / 8;
   const uint64_t base = (uint64_t)(live ? row : 0) * chunks;
-  float h[C][8];
-  v4u wt[C];
+  // every load goes out before any is used; those behind the row read its
+  // last chunk again, and count as zeros
+  v4u xr[C][X_FP32 ? 2 : 1], rr[C], wt[C];
 #pragma unroll
   for (int c = 0; c < C; ++c) {
-    const int i = t0 + c * ROW;
-    if (live && i < chunks) {
-      wt[c] = reinterpret_cast<const v4u*>(P.weight)[i];
-      if constexpr (X_FP32) {
-        const f32x4* x = reinterpret_cast<const f32x4*>(P.x) + 2 * (base + i);
-        const f32x4 lo = x[0], hi = x[1];
+    const int i = t0 + c * ROW < chunks ? t0 + c * ROW : chunks - 1;
+    if constexpr (X_FP32) {
+      const v4u* x = reinterpret_cast<const v4u*>(P.x) + 2 * (base + i);
+      xr[c][0] = x[0];
+      xr[c][1] = x[1];
+    } else {
+      xr[c][0] = reinterpret_cast<const v4u*>(P.x)[base + i];
+    }
+    rr[c] = RESIDUAL ? reinterpret_cast<const v4u*>(P.residual)[base + i] : v4u{0, 0, 0, 0};
+    wt[c] = reinterpret_cast<const v4u*>(P.weight)[i];
+  }
+  float h[C][8];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) h[c][j] = lo[j], h[c][4 + j] = hi[j];
-      } else {
-        unpack8(reinterpret_cast<const v4u*>(P.x)[base + i], h[c]);
+  for (int c = 0; c < C; ++c) {
+    const bool in = t0 + c * ROW < chunks;
+    if constexpr (X_FP32) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        h[c][j] = __uint_as_float(xr[c][0][j]);
+        h[c][4 + j] = __uint_as_float(xr[c][1][j]);
       }
     } else {
-      wt[c] = v4u{0, 0, 0, 0};
-#pragma unroll
-      for (int j = 0; j < 8; ++j) h[c][j] = 0.0f;
+      unpack8(xr[c][0], h[c]);
     }
-  }
-  if (P.residual) {
+    if constexpr (RESIDUAL) {
+      float r[8];
+      unpack8(rr[c], r);
 #pragma unroll
-    for (int c = 0; c < C; ++c) {
-      const int i = t0 + c * ROW;
-      if (live && i < chunks) {
-        float r[8];
-        unpack8(reinterpret_cast<const v4u*>(P.residual)[base + i], r);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) h[c][j] += r[j];
-      }
+      for (int j = 0; j < 8; ++j) h[c][j] += r[j];
     }
+#pragma unroll
+    for (int j = 0; j < 8; ++j) h[c][j] = in ? h[c][j] : 0.0f;
   }
   float sum = 0.0f;
 #pragma unroll
@@ -121,32 +128,38 @@ __global__ void __launch_bounds__(ROW < 256 ? 256 : ROW) norm_kernel(const NormP
   }
 }
 
-template <int ROW, int C, bool X_FP32>
+template <int ROW, int C, bool X_FP32, bool RESIDUAL>
 hipError_t launch(const NormParams& p, hipStream_t stream) {
   constexpr int BLOCK = ROW < 256 ? 256 : ROW, ROWS = BLOCK / ROW;
   const unsigned blocks = (unsigned)(((int64_t)p.num_tokens + ROWS - 1) / ROWS);
-  if (p.out_fp8) norm_kernel<ROW, C, X_FP32, true><<<blocks, BLOCK, 0, stream>>>(p);
-  else norm_kernel<ROW, C, X_FP32, false><<<blocks, BLOCK, 0, stream>>>(p);
+  if (p.out_fp8) norm_kernel<ROW, C, X_FP32, RESIDUAL, true><<<blocks, BLOCK, 0, stream>>>(p);
+  else norm_kernel<ROW, C, X_FP32, RESIDUAL, false><<<blocks, BLOCK, 0, stream>>>(p);
   return hipGetLastError();
 }
 
-template <bool X_FP32>
+template <bool X_FP32, bool RESIDUAL>
 hipError_t launch_x(const NormParams& p, hipStream_t stream) {
   const int chunks = p.hidden / 8;
-  if (chunks <= 64) return launch<64, 1, X_FP32>(p, stream);
-  if (chunks <= 128) return launch<64, 2, X_FP32>(p, stream);
-  if (chunks <= 256) return launch<256, 1, X_FP32>(p, stream);
-  if (chunks <= 512) return launch<256, 2, X_FP32>(p, stream);
-  if (chunks <= 1024) return launch<256, 4, X_FP32>(p, stream);
-  if (chunks <= 2048) return launch<512, 4, X_FP32>(p, stream);
-  return launch<1024, 4, X_FP32>(p, stream);
+  if (chunks <= 64) return launch<64, 1, X_FP32, RESIDUAL>(p, stream);
+  if (chunks <= 128) return launch<64, 2, X_FP32, RESIDUAL>(p, stream);
+  if (chunks <= 256) return launch<256, 1, X_FP32, RESIDUAL>(p, stream);
+  // Few rows leave the GPU idle: more threads a row, fewer chunks a thread.
+  if (p.num_tokens <= kFewTokens && chunks <= 1024)
+    return chunks <= 512 ? launch<512, 1, X_FP32, RESIDUAL>(p, stream)
+                         : launch<1024, 1, X_FP32, RESIDUAL>(p, stream);
+  if (chunks <= 512) return launch<256, 2, X_FP32, RESIDUAL>(p, stream);
+  if (chunks <= 1024) return launch<256, 4, X_FP32, RESIDUAL>(p, stream);
+  if (chunks <= 2048) return launch<512, 4, X_FP32, RESIDUAL>(p, stream);
+  return launch<1024, 4, X_FP32, RESIDUAL>(p, stream);
 }
 
 }  // namespace
 
 hipError_t launch_norm(const NormParams& p, hipStream_t stream) {
   if (p.num_tokens == 0) return hipSuccess;
-  return p.x_fp32 ? launch_x<true>(p, stream) : launch_x<false>(p, stream);
+  if (p.residual)
+    return p.x_fp32 ? launch_x<true, true>(p, stream) : launch_x<false, true>(p, stream);
+  return p.x_fp32 ? launch_x<true, false>(p, stream) : launch_x<false, false>(p, stream);
 }
 
 }  // namespace llmoe

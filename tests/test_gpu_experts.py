@@ -316,6 +316,19 @@ def test_two_calls_at_once(c):
     b.check()
 
 
+def test_strided_and_host_tensors_are_refused():
+    g = Gemm("bf16", [3], 4, 16, 16)
+    for name in ("a", "w", "out"):
+        keep = getattr(g, name)
+        for bad in (torch.cat([keep, keep], -1)[..., ::2], keep.cpu()):
+            setattr(g, name, bad)
+            with pytest.raises(ll.LLMoEError) as ei:
+                g.run()
+            assert ei.value.status == ll.INVALID_ARGUMENT
+        setattr(g, name, keep)
+    g.run().check()
+
+
 # ---- the norm ---------------------------------------------------------------
 
 NORM_SHAPES = [(1, 8), (3, 24), (5, 512), (4, 520), (7, 1024), (9, 1000), (2, 2048), (130, 2056), (3, 4096),
