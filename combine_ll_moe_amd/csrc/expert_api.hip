@@ -50,7 +50,7 @@ bool gemm_sizes(int max_tokens, int n, int k, int num_experts, int act) {
 constexpr int kFewRowsMost = 64;
 
 int launch_gemm(const GemmParams& p, hipStream_t stream) {
-  if (p.max_tokens <= 128 || p.weight == kWeightInt4)
+  if (p.max_tokens <= 128)
     return from_hip(launch_gemm_few(p, INT32_MAX, stream));
   const hipError_t e = launch_gemm_few(p, kFewRowsMost, stream);
   return from_hip(e != hipSuccess ? e : launch_gemm_tile(p, kFewRowsMost, stream));

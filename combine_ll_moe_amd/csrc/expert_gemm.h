@@ -40,13 +40,31 @@ inline uint32_t tile_prefix_bytes(int num_experts) {
   return ((uint32_t)(2 * num_experts + 1) * 4u + 15u) & ~15u;
 }
 
-// Row tiles before each expert: pre[e], e <= E, with ceil(rows / tile_rows)
-// tiles for an expert with `least` < rows <= `most` and none for the others
-// (they are another launch's); the rows of each expert behind them. All
-// THREADS threads call it; scan: one word a wavefront.
-template <int THREADS>
-__device__ __forceinline__ void tile_prefix(const GemmParams& P, int tile_rows, int least, int most,
-                                            uint32_t* pre, uint32_t* scan) {
+// Who takes which rows. An expert with at most `most` rows is the few kernel's,
+// in tiles of kFewRows; of one with more the tile kernel takes tiles of
+// kTileRows, and the few kernel the rows behind the last whole one if they
+// fit in one of its own.
+constexpr int kFewRows = 64;
+constexpr int kTileRows = 256;
+__host__ __device__ __forceinline__ int few_first(int rows, int most) {
+  return rows <= most ? 0 : rows - rows % kTileRows;
+}
+__host__ __device__ __forceinline__ int few_tiles(int rows, int most) {
+  if (rows <= 0) return 0;
+  if (rows <= most) return (rows - 1) / kFewRows + 1;
+  const int left = rows % kTileRows;
+  return left > 0 && left <= kFewRows;
+}
+__host__ __device__ __forceinline__ int big_tiles(int rows, int most) {
+  return rows <= most ? 0 : rows / kTileRows + (rows % kTileRows > kFewRows);
+}
+
+// Row tiles before each expert: pre[e], e <= E, of the few kernel or of the
+// tile kernel; the rows of each expert behind them. All THREADS threads call
+// it; scan: one word a wavefront.
+template <int THREADS, bool FEW>
+__device__ __forceinline__ void tile_prefix(const GemmParams& P, int most, uint32_t* pre,
+                                            uint32_t* scan) {
   const int tid = threadIdx.x, lane = tid & 63, E = P.num_experts;
   const int run = (E + THREADS - 1) / THREADS;
   const int e0 = tid * run < E ? tid * run : E, e1 = e0 + run < E ? e0 + run : E;
@@ -54,7 +72,7 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, int tile_rows, 
   for (int e = e0; e < e1; ++e) {
     int c = P.counts[e];
     c = c < P.max_tokens ? c : P.max_tokens;
-    const uint32_t t = c > least && c <= most ? (uint32_t)((c - 1) / tile_rows + 1) : 0u;
+    const uint32_t t = (uint32_t)(FEW ? few_tiles(c, most) : big_tiles(c, most));
     pre[e] = sum;
     pre[E + 1 + e] = (uint32_t)c;
     sum += t;
@@ -118,6 +136,27 @@ __device__ __forceinline__ Bf16x16 fp8_to_bf16(v4u v) {
           __builtin_bit_cast(bf16x8, v4u{o[4], o[5], o[6], o[7]})};
 }
 
+// Eight codes of a word as bf16 16 + c, in the order 0 4 1 5 2 6 3 7. The two
+// constants come in registers: an and-or takes no literals, and with literals
+// each would be two instructions.
+struct CodeMasks {
+  uint32_t keep, base;
+  __device__ CodeMasks() : keep(0x00780078u), base(0x41804180u) {
+    asm("" : "+s"(keep), "+v"(base));
+  }
+};
+__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w, const CodeMasks& c) {
+  const v4u v = {((w << 3) & c.keep) | c.base, ((w >> 1) & c.keep) | c.base,
+                 ((w >> 5) & c.keep) | c.base, ((w >> 9) & c.keep) | c.base};
+  return __builtin_bit_cast(bf16x8, v);
+}
+// Eight bf16 of A in that order.
+__device__ __forceinline__ bf16x8 a_like_codes(v4u a) {
+  const v4u v = {__builtin_amdgcn_perm(a.z, a.x, 0x05040100u), __builtin_amdgcn_perm(a.z, a.x, 0x07060302u),
+                 __builtin_amdgcn_perm(a.w, a.y, 0x05040100u), __builtin_amdgcn_perm(a.w, a.y, 0x07060302u)};
+  return __builtin_bit_cast(bf16x8, v);
+}
+
 // silu(g) * u in fp32. exp(-g) overflows to infinity for g below about -88:
 // the quotient is then -0, which is silu's limit.
 __device__ __forceinline__ float silu_mul(float g, float u) {
@@ -138,8 +177,8 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float p0, float p1, float p2, flo
   return ((uint32_t)w & ~m) | (0x7F7F7F7Fu & m);
 }
 
-// Rows of experts with at most `most` rows; of experts with more than `least`.
+// Each takes its rows of every expert (few_tiles, big_tiles).
 hipError_t launch_gemm_few(const GemmParams& p, int most, hipStream_t stream);
-hipError_t launch_gemm_tile(const GemmParams& p, int least, hipStream_t stream);
+hipError_t launch_gemm_tile(const GemmParams& p, int most, hipStream_t stream);
 
 }  // namespace llmoe

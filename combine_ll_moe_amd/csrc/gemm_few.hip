@@ -35,7 +35,6 @@ namespace {
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset behind every descriptor's range
-constexpr int kFewRows = 64;      // rows of a tile
 constexpr int kFewFrags = 4;      // weight strips a wavefront holds at once
 constexpr int kFewWaves = 4;      // of a workgroup
 // From this many strips a wavefront (in units of what it holds at once) on,
@@ -209,27 +208,6 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
       load(s, c + (s + D) * WK);
     }
   }
-}
-
-// Eight codes of a word as bf16 16 + c, in the order 0 4 1 5 2 6 3 7. The two
-// constants come in registers: an and-or takes no literals, and with literals
-// each would be two instructions.
-struct CodeMasks {
-  uint32_t keep, base;
-  __device__ CodeMasks() : keep(0x00780078u), base(0x41804180u) {
-    asm("" : "+s"(keep), "+v"(base));
-  }
-};
-__device__ __forceinline__ bf16x8 codes_bf16(uint32_t w, const CodeMasks& c) {
-  const v4u v = {((w << 3) & c.keep) | c.base, ((w >> 1) & c.keep) | c.base,
-                 ((w >> 5) & c.keep) | c.base, ((w >> 9) & c.keep) | c.base};
-  return __builtin_bit_cast(bf16x8, v);
-}
-// Eight bf16 of A in that order.
-__device__ __forceinline__ bf16x8 a_like_codes(v4u a) {
-  const v4u v = {__builtin_amdgcn_perm(a.z, a.x, 0x05040100u), __builtin_amdgcn_perm(a.z, a.x, 0x07060302u),
-                 __builtin_amdgcn_perm(a.w, a.y, 0x05040100u), __builtin_amdgcn_perm(a.w, a.y, 0x07060302u)};
-  return __builtin_bit_cast(bf16x8, v);
 }
 
 // Four words of four lane quarters transposed: word j of quarter q becomes
@@ -772,8 +750,9 @@ __device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it
 // The units [u0, u1) of a list of `tiles` x `units`. A unit is an output
 // strip, or (fp8 out, where a row's 128 columns share a scale) 128 columns.
 template <int WEIGHT, int G, bool GATED, bool OUT_FP8, bool SPLIT>
-__device__ __forceinline__ void do_run(const GemmParams& P, const uint32_t* pre, float* part,
-                                       uint8_t* abuf, int units, uint64_t u0, uint64_t u1) {
+__device__ __forceinline__ void do_run(const GemmParams& P, int most, const uint32_t* pre,
+                                       float* part, uint8_t* abuf, int units, uint64_t u0,
+                                       uint64_t u1) {
   constexpr int SF = GATED ? kFewFrags / 2 : kFewFrags;
   if (u0 >= u1) return;
   // division in 32 bits wherever the list allows it
@@ -793,8 +772,9 @@ __device__ __forceinline__ void do_run(const GemmParams& P, const uint32_t* pre,
     const int c = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + e]);
     Item it;
     it.e = e;
-    it.row0 = (int64_t)e * P.max_tokens + (int64_t)t * kFewRows;
-    it.rows = c - t * kFewRows < kFewRows ? c - t * kFewRows : kFewRows;
+    const int first = few_first(c, most) + t * kFewRows;
+    it.row0 = (int64_t)e * P.max_tokens + first;
+    it.rows = c - first < kFewRows ? c - first : kFewRows;
     it.a = P.a + (uint64_t)it.row0 * P.k * (WEIGHT == kWeightFp8 ? 1 : 2);
     it.a_scales = WEIGHT == kWeightFp8 ? P.a_scales + (uint64_t)it.row0 * (P.k / 128) : nullptr;
     int here = units - unit;
@@ -833,7 +813,7 @@ __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmP
   __shared__ __align__(16) float part[kFewWaves * kPartFloats];
   __shared__ __align__(16) uint8_t abuf[2 * kFewRows * 2 * step_columns<WEIGHT>];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
-  tile_prefix<kFewWaves * 64>(P, kFewRows, 0, most, pre, scan);
+  tile_prefix<kFewWaves * 64, true>(P, most, pre, scan);
   const uint32_t tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
   const int units = OUT_FP8 ? P.n / 128 : (P.n + 15) / 16;
   const uint64_t total = (uint64_t)tiles * units;
@@ -843,9 +823,9 @@ __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmP
   const uint32_t at = (blockIdx.x % kXcds << LOG) / kXcds + blockIdx.x / kXcds;
   const uint64_t u0 = total * at >> LOG, u1 = total * (at + 1) >> LOG;
   if (OUT_FP8 || total >> LOG >= kFewLong * (GATED ? kFewFrags / 2 : kFewFrags))
-    do_run<WEIGHT, G, GATED, OUT_FP8, false>(P, pre, part, abuf, units, u0, u1);
+    do_run<WEIGHT, G, GATED, OUT_FP8, false>(P, most, pre, part, abuf, units, u0, u1);
   else
-    do_run<WEIGHT, G, GATED, OUT_FP8, true>(P, pre, part, abuf, units, u0, u1);
+    do_run<WEIGHT, G, GATED, OUT_FP8, true>(P, most, pre, part, abuf, units, u0, u1);
 }
 
 template <int WEIGHT, int G, bool GATED, bool OUT_FP8>

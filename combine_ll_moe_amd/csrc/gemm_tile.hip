@@ -30,7 +30,7 @@ namespace {
 
 typedef __amdgpu_buffer_rsrc_t Rsrc;
 constexpr uint32_t kOutside = 0x7FFFFFF0u;
-constexpr int kTile = 256;            // rows of a tile, and weight rows
+constexpr int kTile = kTileRows;      // rows of a tile, and weight rows
 constexpr int kStepBytes = 128;       // of a row in a k step
 constexpr int kHalf = kTile * kStepBytes;
 constexpr int kThreads = 512;
@@ -48,7 +48,6 @@ struct Source {
   uint32_t a_off, w_off;  // this lane's first row and chunk
   uint32_t ld;            // row bytes
   uint32_t chunk;         // byte of this lane's chunk in a step
-  uint32_t w_jump;        // bytes from W's tile row 128 as it would be to where it is
 };
 
 __device__ __forceinline__ void copy_step(const Source& s, int step, uint8_t* lds, int wave) {
@@ -138,14 +137,39 @@ __device__ __forceinline__ void multiply(const uint8_t* lds, int wm, int wn, con
   }
 }
 
+// One tile: rows [row0, row0 + rows) of expert e, output columns [col0, col0 +
+// cols). An expert's tiles go four tile columns at a time, all its row tiles.
+struct Tile {
+  int e, rows, col0, cols;
+  int64_t row0;
+};
+template <int COLS>
+__device__ __forceinline__ Tile tile_at(const GemmParams& P, const uint32_t* pre, uint64_t t, int across) {
+  Tile o;
+  o.e = __builtin_amdgcn_readfirstlane(expert_of_tile(pre, P.num_experts, (uint32_t)(t / across)));
+  const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[o.e]);
+  const uint32_t down = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[o.e + 1]) - first;
+  const uint64_t in_e = t - (uint64_t)first * across;
+  const int group = (int)(in_e / (4ull * down));
+  const int wide = across - 4 * group < 4 ? across - 4 * group : 4;
+  const int in_g = (int)(in_e - 4ull * down * group);
+  const int rt = in_g / wide, ct = 4 * group + in_g % wide;
+  const int left = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + o.e]) - rt * kTile;
+  o.rows = left < kTile ? left : kTile;
+  o.row0 = (int64_t)o.e * P.max_tokens + (int64_t)rt * kTile;
+  o.col0 = ct * COLS;
+  o.cols = P.n - o.col0 < COLS ? P.n - o.col0 : COLS;
+  return o;
+}
+
 template <int WEIGHT, bool GATED, bool OUT_FP8>
-__global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams P, int least) {
+__global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams P, int most) {
   extern __shared__ __align__(16) uint8_t lds_raw[];
   __shared__ uint32_t scan[kThreads / 64];
   __shared__ __align__(16) uint8_t step0[2 * kHalf];
   __shared__ __align__(16) uint8_t step1[2 * kHalf];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
-  tile_prefix<kThreads>(P, kTile, least, INT32_MAX, pre, scan);
+  tile_prefix<kThreads, false>(P, most, pre, scan);
   const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -163,21 +187,9 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
   const uint64_t x = blockIdx.x % kXcds, per = gridDim.x / kXcds;
   const uint64_t t0 = tiles * x / kXcds, t1 = tiles * (x + 1) / kXcds;
   for (uint64_t t = t0 + blockIdx.x / kXcds; t < t1; t += per) {
-    // an expert's tiles: four tile columns at a time, all its row tiles
-    const int e = __builtin_amdgcn_readfirstlane(
-        expert_of_tile(pre, P.num_experts, (uint32_t)(t / across)));
-    const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e]);
-    const uint32_t down = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e + 1]) - first;
-    const uint64_t in_e = t - (uint64_t)first * across;
-    const int group = (int)(in_e / (4ull * down));
-    const int wide = across - 4 * group < 4 ? across - 4 * group : 4;
-    const int in_g = (int)(in_e - 4ull * down * group);
-    const int rt = in_g / wide, ct = 4 * group + in_g % wide;
-    int rows = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + e]) - rt * kTile;
-    rows = rows < kTile ? rows : kTile;
-    const int64_t row0 = (int64_t)e * P.max_tokens + (int64_t)rt * kTile;
-    const int col0 = ct * COLS;
-    const int cols = P.n - col0 < COLS ? P.n - col0 : COLS;
+    const Tile tile = tile_at<COLS>(P, pre, t, across);
+    const int e = tile.e, rows = tile.rows, col0 = tile.col0, cols = tile.cols;
+    const int64_t row0 = tile.row0;
 
     Source s;
     s.ld = ld;
@@ -282,7 +294,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
           const float amax = fmaxf(most[row * 2], most[row * 2 + 1]);
           inv = amax > 0.0f ? 448.0f / amax : 0.0f;
           if (wn == 0 && hi == 0)
-            P.out_scales[orow * (P.n / 128) + ct] = amax > 0.0f ? amax / 448.0f : 0.0f;
+            P.out_scales[orow * (P.n / 128) + col0 / 128] = amax > 0.0f ? amax / 448.0f : 0.0f;
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {
@@ -303,23 +315,236 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
   }
 }
 
+// The same tiles with 4-bit weights. A k step is 64 columns: 32 KiB of A and
+// 8 KiB of codes. The sums of a step (of half a step for groups of 32) are
+// scaled and added up as gemm_few.hip does; sum x comes from one product with
+// ones a fragment of rows. Scales and zero points of the tile's 256 weight rows
+// come in blocks of 8 groups into a ring of four blocks a row: a window of 8
+// groups reads two of them, starting anywhere in the first, while the block
+// behind the next window's first is written.
+constexpr int kRing = 80, kZeroRing = 40;  // LDS bytes of a row, spread over the banks
+
+template <int G, bool GATED>
+__global__ void __launch_bounds__(kThreads, 2) gemm_tile_int4_kernel(const GemmParams P, int most) {
+  extern __shared__ __align__(16) uint8_t lds_raw[];
+  __shared__ uint32_t scan[kThreads / 64];
+  __shared__ __align__(16) uint8_t a0[kHalf], a1[kHalf], w0[kTile * 32], w1[kTile * 32];
+  __shared__ __align__(16) uint8_t ring[kTile * (kRing + kZeroRing)];
+  uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
+  tile_prefix<kThreads, false>(P, most, pre, scan);
+  const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  constexpr int COLS = GATED ? 128 : 256;
+  constexpr int GROUPS = G == 32 ? 2 : 1;  // sums of a step that are scaled apart
+  const int across = (P.n + COLS - 1) / COLS;
+  const uint32_t row_tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
+  const uint64_t tiles = (uint64_t)row_tiles * across;
+  const uint32_t lda = (uint32_t)P.k * 2, ldw = (uint32_t)P.k / 2;
+  const int steps = (P.k + 63) / 64, groups = P.k / G;
+  const int rows_w = (GATED ? 2 : 1) * P.n;
+  const uint32_t values = (uint32_t)rows_w * groups;
+  const float z_none = P.w_zeros ? 16.0f : 24.0f;
+  const CodeMasks masks;
+  const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
+  const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
+  const f32x4 zero = {0, 0, 0, 0};
+
+  const uint64_t x = blockIdx.x % kXcds, per = gridDim.x / kXcds;
+  const uint64_t t0 = tiles * x / kXcds, t1 = tiles * (x + 1) / kXcds;
+  for (uint64_t t = t0 + blockIdx.x / kXcds; t < t1; t += per) {
+    const Tile tile = tile_at<COLS>(P, pre, t, across);
+    const int rows = tile.rows, col0 = tile.col0, cols = tile.cols;
+    const Rsrc ra = rsrc_of(P.a + (uint64_t)tile.row0 * lda, (uint32_t)rows * lda);
+    const uint64_t w_row = (uint64_t)tile.e * rows_w + col0;
+    const bool up = GATED && wave >= 4;  // wavefronts 4-7 copy the up rows
+    const Rsrc rw = rsrc_of(P.w + (w_row + (up ? P.n : 0)) * ldw, (uint32_t)cols * ldw);
+    const uint32_t ar = (uint32_t)wave * 32 + (lane >> 3), achunk = (uint32_t)((lane & 7) ^ (ar & 7)) * 16;
+    // codes: 32 rows an instruction, two lanes a row; a row's halves change
+    // places with bit 3 of the row, for the banks
+    const uint32_t wr = (uint32_t)wave * 32 + (lane >> 1);
+    const uint32_t whalf = (uint32_t)((lane & 1) ^ (wr >> 3 & 1)) * 16;
+    const uint32_t w_off = (up ? wr - 128 : wr) * ldw;
+    auto copy = [&](int step, uint8_t* ta, uint8_t* tw) {
+      const uint32_t at = (uint32_t)step * 128 + achunk;
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        __builtin_amdgcn_raw_ptr_buffer_load_lds(
+            ra, (LdsByte*)(ta + (wave * 32 + i * 8) * kStepBytes), 16,
+            at < lda ? (int)((ar + i * 8) * lda + at) : (int)kOutside, 0, 0, 0);
+      const uint32_t wat = (uint32_t)step * 32 + whalf;
+      __builtin_amdgcn_raw_ptr_buffer_load_lds(rw, (LdsByte*)(tw + wave * 32 * 32), 16,
+                                               wat < ldw ? (int)(w_off + wat) : (int)kOutside, 0, 0, 0);
+    };
+
+    // the ring: thread i < 256 brings in tile row i's blocks
+    const Rsrc rs = rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)tile.e * values, 2 * values);
+    const Rsrc rz = rsrc_of(P.w_zeros + (P.w_zeros ? (uint64_t)tile.e * values : 0), P.w_zeros ? values : 0u);
+    auto weight_row = [&](int i) { return col0 + (GATED && i >= 128 ? P.n + i - 128 : i); };
+    uint32_t block = 2 * (uint32_t)weight_row(tid & 255) * groups & ~15u;
+    uint32_t zblock = (uint32_t)weight_row(tid & 255) * groups & ~7u;
+    v4u next = {0, 0, 0, 0};
+    v2u znext = {0, 0};
+    auto fetch = [&] {
+      next = __builtin_amdgcn_raw_buffer_load_b128(rs, (int)block, 0, 0);
+      znext = __builtin_amdgcn_raw_buffer_load_b64(rz, (int)zblock, 0, 0);
+      block += 16;
+      zblock += 8;
+    };
+    auto put = [&](int b) {
+      *reinterpret_cast<v4u*>(ring + tid * kRing + (b & 3) * 16) = next;
+      *reinterpret_cast<v2u*>(ring + kTile * kRing + tid * kZeroRing + (b & 3) * 8) = znext;
+    };
+    // this lane's row of each fragment: LDS place and phase
+    uint32_t r_at[8], r_phase[8];
+#pragma unroll
+    for (int f = 0; f < 8; ++f) {
+      const int i = frag_row<GATED>(wn, f) + lo;
+      r_at[f] = (uint32_t)i;
+      r_phase[f] = (uint32_t)weight_row(i) * groups & 7;
+    }
+
+    f32x4 acc[4][8];
+#pragma unroll
+    for (int m = 0; m < 4; ++m)
+#pragma unroll
+      for (int f = 0; f < 8; ++f) acc[m][f] = zero;
+    const bool busy = wm * 64 < rows;
+
+    auto multiply4 = [&](int step, const uint8_t* la, const uint8_t* lw) __attribute__((always_inline)) {
+      bf16x8 a[4][2];
+      f32x4 sum[4][GROUPS];
+#pragma unroll
+      for (int m = 0; m < 4; ++m)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          a[m][j] = a_like_codes(chunk_of(la, wm * 64 + m * 16 + lo, 4 * j + hi));
+          const int u = GROUPS == 2 ? j : 0;
+          sum[m][u] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+              a[m][j], ones, GROUPS == 2 || j == 0 ? zero : sum[m][u], 0, 0, 0);
+        }
+#pragma unroll
+      for (int f = 0; f < 8; ++f) {
+        const int r = frag_row<GATED>(wn, f) + lo;
+#pragma unroll
+        for (int u = 0; u < GROUPS; ++u) {
+          f32x4 p[4];
+#pragma unroll
+          for (int j = u; j < (GROUPS == 2 ? u + 1 : 2); ++j) {
+            const uint32_t w = *reinterpret_cast<const uint32_t*>(lw + r * 32 + ((j ^ (r >> 3 & 1)) << 4) + hi * 4);
+            const bf16x8 wf = codes_bf16(w, masks);
+#pragma unroll
+            for (int m = 0; m < 4; ++m)
+              p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m][j], wf, j == u ? zero : p[m], 0, 0, 0);
+          }
+          const int g = G == 128 ? step >> 1 : step * GROUPS + u;
+          const uint32_t at = r_phase[f] + (uint32_t)g;
+          const float read = __uint_as_float(
+              (uint32_t) * reinterpret_cast<const uint16_t*>(ring + r_at[f] * kRing + (2 * at & 63)) << 16);
+          const float sc = G == 128 || g < groups ? read : 0.0f;
+          const float off = z_none + (float)ring[kTile * kRing + r_at[f] * kZeroRing + (at & 31)];
+#pragma unroll
+          for (int m = 0; m < 4; ++m)
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              acc[m][f][q] = __builtin_fmaf(sc, __builtin_fmaf(-off, sum[m][u][q], p[m][q]), acc[m][f][q]);
+        }
+        if (f & 1) __builtin_amdgcn_sched_barrier(0);  // fragments in turn, for the registers
+      }
+    };
+    // a window of 8 groups starts: the block behind the next window's first
+    constexpr int WINDOW = 8 * G / 64;  // steps
+    auto enter = [&](int step) {
+      if (step % WINDOW == 0 && wave < 4) {
+        put(step / WINDOW + 2);
+        fetch();
+      }
+    };
+
+    copy(0, a0, w0);
+    if (wave < 4) {
+      fetch();
+      put(0);
+      fetch();
+      put(1);
+      fetch();
+    }
+    __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+    __syncthreads();
+    for (int k = 0; k < steps; k += 2) {
+      enter(k);
+      if (k + 1 < steps) copy(k + 1, a1, w1);
+      if (busy) multiply4(k, a0, w0);
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      __syncthreads();
+      if (k + 1 >= steps) break;
+      if (k + 2 < steps) copy(k + 2, a0, w0);
+      if (busy) multiply4(k + 1, a1, w1);
+      __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
+      __syncthreads();
+    }
+
+    // outputs: 16 rows of a wavefront pass through LDS, four columns a lane
+    constexpr int F = GATED ? 4 : 8, LD = F * 16;
+    static_assert(4 * 16 * LD * 4 <= kHalf, "four wavefronts a buffer");
+    float* mine = reinterpret_cast<float*>(wave < 4 ? a0 : a1) + (wave & 3) * 16 * LD;
+#pragma unroll
+    for (int m = 0; m < 4; ++m) {
+#pragma unroll
+      for (int f = 0; f < F; ++f)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          float v = acc[m][f][q];
+          if constexpr (GATED) v = silu_mul(v, acc[m][f + 4][q]);
+          mine[(4 * hi + q) * LD + f * 16 + lo] = v;
+        }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int i = lane; i < 16 * F * 4; i += 64) {
+        const int r = i / (F * 4), c = 4 * (i % (F * 4)), row = wm * 64 + m * 16 + r;
+        const int col = wn * F * 16 + c;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(mine + r * LD + c);
+        if (row < rows && col < cols)
+          *reinterpret_cast<uint2*>(P.out + 2 * ((uint64_t)(tile.row0 + row) * P.n + col0 + col)) =
+              make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+      }
+      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+      __builtin_amdgcn_wave_barrier();
+    }
+    __syncthreads();  // the buffers are free for the next tile
+  }
+}
+
+template <int G>
+hipError_t launch_int4(const GemmParams& p, int most, hipStream_t stream) {
+  const uint32_t lds = tile_prefix_bytes(p.num_experts);
+  if (p.gated) gemm_tile_int4_kernel<G, true><<<256, kThreads, lds, stream>>>(p, most);
+  else gemm_tile_int4_kernel<G, false><<<256, kThreads, lds, stream>>>(p, most);
+  return hipGetLastError();
+}
+
 template <int WEIGHT, bool GATED, bool OUT_FP8>
-hipError_t launch(const GemmParams& p, int least, hipStream_t stream) {
+hipError_t launch(const GemmParams& p, int most, hipStream_t stream) {
   gemm_tile_kernel<WEIGHT, GATED, OUT_FP8>
-      <<<256, kThreads, tile_prefix_bytes(p.num_experts), stream>>>(p, least);
+      <<<256, kThreads, tile_prefix_bytes(p.num_experts), stream>>>(p, most);
   return hipGetLastError();
 }
 
 }  // namespace
 
-hipError_t launch_gemm_tile(const GemmParams& p, int least, hipStream_t stream) {
+hipError_t launch_gemm_tile(const GemmParams& p, int most, hipStream_t stream) {
   if (p.weight == kWeightFp8) {
-    if (p.out_fp8) return launch<kWeightFp8, true, true>(p, least, stream);
-    return p.gated ? launch<kWeightFp8, true, false>(p, least, stream)
-                   : launch<kWeightFp8, false, false>(p, least, stream);
+    if (p.out_fp8) return launch<kWeightFp8, true, true>(p, most, stream);
+    return p.gated ? launch<kWeightFp8, true, false>(p, most, stream)
+                   : launch<kWeightFp8, false, false>(p, most, stream);
   }
-  return p.gated ? launch<kWeightBf16, true, false>(p, least, stream)
-                 : launch<kWeightBf16, false, false>(p, least, stream);
+  if (p.weight == kWeightInt4)
+    return p.group == 128  ? launch_int4<128>(p, most, stream)
+           : p.group == 64 ? launch_int4<64>(p, most, stream)
+                           : launch_int4<32>(p, most, stream);
+  return p.gated ? launch<kWeightBf16, true, false>(p, most, stream)
+                 : launch<kWeightBf16, false, false>(p, most, stream);
 }
 
 }  // namespace llmoe
