@@ -59,6 +59,22 @@ __host__ __device__ __forceinline__ int big_tiles(int rows, int most) {
   return rows <= most ? 0 : rows / kTileRows + (rows % kTileRows > kFewRows);
 }
 
+// Inclusive sums over a wavefront's lanes, in DPP steps (by 1, 2, 4, 8 lanes
+// within rows of 16, then the rows' totals): a few cycles each, where a step
+// through LDS takes a hundred.
+template <int CTRL, int ROWS, int BANKS>
+__device__ __forceinline__ uint32_t dpp_add(uint32_t v) {
+  return v + (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, ROWS, BANKS, false);
+}
+__device__ __forceinline__ uint32_t wave_sums(uint32_t v) {
+  v = dpp_add<0x111, 0xF, 0xF>(v);  // row_shr:1
+  v = dpp_add<0x112, 0xF, 0xF>(v);  // row_shr:2
+  v = dpp_add<0x114, 0xF, 0xE>(v);  // row_shr:4
+  v = dpp_add<0x118, 0xF, 0xC>(v);  // row_shr:8
+  v = dpp_add<0x142, 0xA, 0xF>(v);  // row_bcast:15
+  return dpp_add<0x143, 0xC, 0xF>(v);  // row_bcast:31
+}
+
 // Row tiles before each expert: pre[e], e <= E, of the few kernel or of the
 // tile kernel; the rows of each expert behind them. All THREADS threads call
 // it; scan: one word a wavefront.
@@ -77,12 +93,7 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, int most, uint3
     pre[E + 1 + e] = (uint32_t)c;
     sum += t;
   }
-  uint32_t incl = sum;
-#pragma unroll
-  for (int d = 1; d < 64; d <<= 1) {
-    const uint32_t o = __shfl_up(incl, d, 64);
-    if (lane >= d) incl += o;
-  }
+  const uint32_t incl = wave_sums(sum);
   if (lane == 63) scan[tid / 64] = incl;
   __syncthreads();
   uint32_t base = incl - sum;
@@ -92,16 +103,18 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, int most, uint3
   __syncthreads();
 }
 
-// Expert of tile t < pre[E]: the largest e with pre[e] <= t. An expert
-// without tiles has pre[e] == pre[e + 1] and is never the answer.
+// Expert of tile t < pre[E]: as many as have their last tile before t. All
+// lanes of a wavefront look, 64 experts at a time (E <= 4096: at most twice);
+// the answer is the same for all.
 __device__ __forceinline__ int expert_of_tile(const uint32_t* pre, int E, uint32_t t) {
-  int lo = 0, hi = E - 1;
-  while (lo < hi) {
-    const int mid = (lo + hi + 1) >> 1;
-    if (pre[mid] <= t) lo = mid;
-    else hi = mid - 1;
+  const int lane = threadIdx.x & 63;
+  int base = 0;
+  if (E > 64) {
+    const int run = (E + 63) / 64, last = (lane + 1) * run;
+    base = run * __popcll(__ballot(last < E && pre[last < E ? last : E] <= t));
   }
-  return lo;
+  const int e = base + lane;
+  return base + __popcll(__ballot(e < E && pre[e < E ? e + 1 : E] <= t));
 }
 
 typedef float f32x4 __attribute__((ext_vector_type(4)));

@@ -40,9 +40,10 @@ constexpr int kFewWaves = 4;      // of a workgroup
 // From this many strips a wavefront (in units of what it holds at once) on,
 // the list is long.
 constexpr int kFewLong = 4;
-constexpr int kPartLd = kFewFrags * 16 + 4;  // floats of a row of partial sums, at most
-constexpr int kPartFloats = 1152;            // a wavefront's 16 rows of them, or its ring of scales
-static_assert(kPartFloats >= 16 * kPartLd);
+// LDS of a workgroup: partial sums, or the wavefronts' rings of scales and
+// the two steps' rows of A.
+constexpr int kRingBytes = 64 * 72;
+constexpr int kPoolBytes = kFewWaves * kRingBytes + 2 * kFewRows * 256;
 
 __device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
@@ -89,7 +90,7 @@ __device__ __forceinline__ int strip_rows(const GemmParams& P, const Item& it, i
 template <int MF, int NF, bool GATED>
 __device__ __forceinline__ void sum_bf16(const GemmParams& P, const Item& it, int kw, int WK,
                                          f32x4 (&acc)[MF][NF]) {
-  constexpr int D = MF == 4 ? 2 : 3;  // chunks in flight
+  constexpr int D = MF + NF <= 5 ? 4 : MF + NF <= 6 ? 3 : 2;  // chunks in flight
   const int lane = threadIdx.x & 63;
   const uint32_t ld = 2u * (uint32_t)P.k;
   const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * ld);
@@ -129,6 +130,7 @@ __device__ __forceinline__ void sum_bf16(const GemmParams& P, const Item& it, in
                 __builtin_bit_cast(bf16x8, ab[s][m][j]), __builtin_bit_cast(bf16x8, wb[s][f][j]),
                 acc[m][f], 0, 0, 0);
       load(s, c + (s + D) * WK);
+      __builtin_amdgcn_sched_barrier(0);  // a stage waits for its own loads, not for the next one's
     }
   }
 }
@@ -206,6 +208,7 @@ __device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int
         }
       }
       load(s, c + (s + D) * WK);
+      __builtin_amdgcn_sched_barrier(0);  // a stage waits for its own loads, not for the next one's
     }
   }
 }
@@ -247,7 +250,7 @@ struct ScaleRing {
   uint32_t at[NF], zat[NF];     // LDS: row f * 16 + lane % 16
   uint32_t phase[NF], zphase[NF];
   float none;
-  static_assert(kBytes <= 4 * kPartFloats);
+  static_assert(kBytes <= kRingBytes);
 
   __device__ __forceinline__ void init(const GemmParams& P, const Item& it, int groups, int first,
                                        uint8_t* ring) {
@@ -628,15 +631,18 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
 // strips beside each other. Sums first, then, 16 rows at a time, they pass
 // through LDS and the outputs go out, four columns a thread.
 template <int WEIGHT, int G, int MF, int NF, bool GATED, bool OUT_FP8, bool SPLIT>
-__device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, float* part,
-                                        uint8_t* abuf) {
-  constexpr bool ALONE = !SPLIT && !OUT_FP8;
+__device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, uint8_t* pool) {
+  constexpr bool ALONE = !SPLIT && !OUT_FP8;  // a wavefront's outputs are its own
   constexpr int WN = OUT_FP8 ? kFewWaves : 1;
   constexpr int PARTS = SPLIT ? kFewWaves : 1;
   constexpr int SF = GATED ? NF / 2 : NF;   // output strips a wavefront
   constexpr int LD = NF * 16 + 4;           // floats of a partial row
   constexpr int COLS = WN * SF * 16;
   constexpr int THREADS = ALONE ? 64 : kFewWaves * 64;
+  // row fragments that pass through LDS at once
+  constexpr int FIT = kPoolBytes / (kFewWaves * 16 * LD * 4);
+  constexpr int MP = FIT >= MF ? MF : FIT >= 2 ? 2 : 1;
+  static_assert(FIT >= 1);
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int tid = ALONE ? lane : threadIdx.x;
@@ -651,10 +657,9 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
   for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-  // a wavefront's ring of scales and, after the sums, its part of them
-  uint8_t* ring = reinterpret_cast<uint8_t*>(part + wave * kPartFloats);
+  uint8_t* ring = pool + wave * kRingBytes;
   if constexpr (!SPLIT)
-    sum_shared<WEIGHT, G, MF, NF, GATED>(P, it, mine, abuf, ring, acc);
+    sum_shared<WEIGHT, G, MF, NF, GATED>(P, it, mine, pool + kFewWaves * kRingBytes, ring, acc);
   else if constexpr (WEIGHT == kWeightBf16)
     sum_bf16<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
   else if constexpr (WEIGHT == kWeightFp8)
@@ -670,29 +675,39 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
       __syncthreads();
     }
   };
+  // the pool was the rings' and A's until here
+  if (!SPLIT || WEIGHT == kWeightInt4) __syncthreads();
   const int lo = lane & 15, hi = lane >> 4;
-  float* mp = part + wave * kPartFloats;
+  constexpr int WAVE = MP * 16 * LD;
+  float* part = reinterpret_cast<float*>(pool);
+  float* mp = part + wave * WAVE;
   const float* first = ALONE ? mp : part;
 #pragma unroll
-  for (int m = 0; m < MF; ++m) {
-    if (m * 16 >= it.rows) break;  // the same for all who meet
+  for (int m0 = 0; m0 < MF; m0 += MP) {
+    if (m0 * 16 >= it.rows) break;  // the same for all who meet
 #pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      if constexpr (WEIGHT == kWeightFp8) {
-        *reinterpret_cast<f32x4*>(mp + lo * LD + f * 16 + 4 * hi) = acc[m][f];
-      } else {
+    for (int m = 0; m < MP; ++m)
 #pragma unroll
-        for (int r = 0; r < 4; ++r) mp[(4 * hi + r) * LD + f * 16 + lo] = acc[m][f][r];
+      for (int f = 0; f < NF; ++f) {
+        float* to = mp + m * 16 * LD + f * 16;
+        if constexpr (WEIGHT == kWeightFp8) {
+          *reinterpret_cast<f32x4*>(to + lo * LD + 4 * hi) = acc[m0 + m][f];
+        } else {
+#pragma unroll
+          for (int r = 0; r < 4; ++r) to[(4 * hi + r) * LD + lo] = acc[m0 + m][f][r];
+        }
       }
-    }
     meet();
-    for (int i = tid; i < 16 * COLS / 4; i += THREADS) {
+    const int rows = it.rows - m0 * 16 < MP * 16 ? it.rows - m0 * 16 : MP * 16;
+    // (fp8 out: whole wavefronts hold rows together, so none leaves early)
+    const int todo = (OUT_FP8 ? MP * 16 : rows) * (COLS / 4);
+    for (int i = tid; i < todo; i += THREADS) {
       const int row = i / (COLS / 4), c4 = 4 * (i % (COLS / 4));
       const int list = c4 / (SF * 16), at = c4 % (SF * 16);
       f32x4 v = {0, 0, 0, 0}, u = {0, 0, 0, 0};
 #pragma unroll
       for (int q = 0; q < PARTS; ++q) {
-        const float* p = first + (SPLIT ? q : list) * kPartFloats + row * LD + at;
+        const float* p = first + (SPLIT ? q : list) * WAVE + row * LD + at;
         v += *reinterpret_cast<const f32x4*>(p);
         if constexpr (GATED) u += *reinterpret_cast<const f32x4*>(p + SF * 16);
       }
@@ -702,8 +717,8 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
       }
       const Item& of = ALONE ? mine : it;
       const int col = of.strip * 16 + c4;
-      const bool in = m * 16 + row < it.rows && col < P.n && c4 < of.strips * 16;
-      const uint64_t orow = (uint64_t)(it.row0 + m * 16 + row);
+      const bool in = row < rows && col < P.n && c4 < of.strips * 16;
+      const uint64_t orow = (uint64_t)(it.row0 + m0 * 16 + row);
       if constexpr (OUT_FP8) {
         // 32 lanes hold a row's 128 columns
         float amax = 0.0f;
@@ -724,26 +739,28 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, flo
     }
     meet();
   }
+  // before the next item's rings: a wavefront's part of the pool was not
+  // where its ring is
+  if (ALONE) __syncthreads();
 }
 
 template <int WEIGHT, int G, int NF, bool GATED, bool OUT_FP8, bool SPLIT>
-__device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it, float* part,
-                                             uint8_t* abuf) {
+__device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it, uint8_t* pool) {
   if (it.rows <= 16) {
-    do_item<WEIGHT, G, 1, NF, GATED, OUT_FP8, SPLIT>(P, it, part, abuf);
+    do_item<WEIGHT, G, 1, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
   } else if (it.rows <= 32) {
-    do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, it, part, abuf);
+    do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
   } else if constexpr (SPLIT && WEIGHT != kWeightBf16 && NF == 4) {
     // registers hold 64 rows of A beside two strips
     constexpr int SF = GATED ? 1 : 2;
     Item half = it;
     half.strips = it.strips < SF ? it.strips : SF;
-    do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, part, abuf);
+    do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, pool);
     half.strip += SF;
     half.strips = it.strips - SF;
-    if (half.strips > 0) do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, part, abuf);
+    if (half.strips > 0) do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, pool);
   } else {
-    do_item<WEIGHT, G, 4, NF, GATED, OUT_FP8, SPLIT>(P, it, part, abuf);
+    do_item<WEIGHT, G, 4, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
   }
 }
 
@@ -751,20 +768,19 @@ __device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it
 // strip, or (fp8 out, where a row's 128 columns share a scale) 128 columns.
 template <int WEIGHT, int G, bool GATED, bool OUT_FP8, bool SPLIT>
 __device__ __forceinline__ void do_run(const GemmParams& P, int most, const uint32_t* pre,
-                                       float* part, uint8_t* abuf, int units, uint64_t u0,
-                                       uint64_t u1) {
+                                       uint8_t* pool, int units, uint64_t u0, uint64_t u1) {
   constexpr int SF = GATED ? kFewFrags / 2 : kFewFrags;
   if (u0 >= u1) return;
   // division in 32 bits wherever the list allows it
   uint32_t tile = u1 >> 32 ? (uint32_t)(u0 / (uint32_t)units) : (uint32_t)u0 / (uint32_t)units;
   int unit = (int)(u0 - (uint64_t)tile * units);
-  int e = __builtin_amdgcn_readfirstlane(expert_of_tile(pre, P.num_experts, tile));
+  int e = expert_of_tile(pre, P.num_experts, tile);
   uint32_t end = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e + 1]);
   for (uint64_t left = u1 - u0; left > 0;) {
     if (unit == units) {
       unit = 0;
       if (++tile == end) {
-        e = __builtin_amdgcn_readfirstlane(expert_of_tile(pre, P.num_experts, tile));
+        e = expert_of_tile(pre, P.num_experts, tile);
         end = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e + 1]);
       }
     }
@@ -784,19 +800,19 @@ __device__ __forceinline__ void do_run(const GemmParams& P, int most, const uint
     if constexpr (OUT_FP8) {
       it.strip = unit * 8;
       it.strips = 8;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, part, abuf);
+      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, pool);
     } else if constexpr (!SPLIT) {
       // as many strips as the workgroup holds, in items of like size
       const int items = (here + kFewWaves * SF - 1) / (kFewWaves * SF);
       it.strips = done = (here + items - 1) / items;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, part, abuf);
+      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, pool);
     } else if (here >= SF) {
       it.strips = done = SF;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, true>(P, it, part, abuf);
+      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, true>(P, it, pool);
     } else {
       // the run's last strips, fewer than a wavefront holds
       it.strips = 1;
-      do_item_rows<WEIGHT, G, GATED ? 2 : 1, GATED, OUT_FP8, true>(P, it, part, abuf);
+      do_item_rows<WEIGHT, G, GATED ? 2 : 1, GATED, OUT_FP8, true>(P, it, pool);
     }
     unit += done;
     left -= done;
@@ -810,8 +826,7 @@ template <int WEIGHT, int G, bool GATED, bool OUT_FP8>
 __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmParams P, int most) {
   extern __shared__ __align__(16) uint8_t lds_raw[];
   __shared__ uint32_t scan[kFewWaves];
-  __shared__ __align__(16) float part[kFewWaves * kPartFloats];
-  __shared__ __align__(16) uint8_t abuf[2 * kFewRows * 2 * step_columns<WEIGHT>];
+  __shared__ __align__(16) uint8_t pool[kPoolBytes];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
   tile_prefix<kFewWaves * 64, true>(P, most, pre, scan);
   const uint32_t tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
@@ -823,9 +838,9 @@ __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmP
   const uint32_t at = (blockIdx.x % kXcds << LOG) / kXcds + blockIdx.x / kXcds;
   const uint64_t u0 = total * at >> LOG, u1 = total * (at + 1) >> LOG;
   if (OUT_FP8 || total >> LOG >= kFewLong * (GATED ? kFewFrags / 2 : kFewFrags))
-    do_run<WEIGHT, G, GATED, OUT_FP8, false>(P, most, pre, part, abuf, units, u0, u1);
+    do_run<WEIGHT, G, GATED, OUT_FP8, false>(P, most, pre, pool, units, u0, u1);
   else
-    do_run<WEIGHT, G, GATED, OUT_FP8, true>(P, most, pre, part, abuf, units, u0, u1);
+    do_run<WEIGHT, G, GATED, OUT_FP8, true>(P, most, pre, pool, units, u0, u1);
 }
 
 template <int WEIGHT, int G, bool GATED, bool OUT_FP8>

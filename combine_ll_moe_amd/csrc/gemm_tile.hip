@@ -146,7 +146,7 @@ struct Tile {
 template <int COLS>
 __device__ __forceinline__ Tile tile_at(const GemmParams& P, const uint32_t* pre, uint64_t t, int across) {
   Tile o;
-  o.e = __builtin_amdgcn_readfirstlane(expert_of_tile(pre, P.num_experts, (uint32_t)(t / across)));
+  o.e = expert_of_tile(pre, P.num_experts, (uint32_t)(t / across));
   const uint32_t first = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[o.e]);
   const uint32_t down = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[o.e + 1]) - first;
   const uint64_t in_e = t - (uint64_t)first * across;
