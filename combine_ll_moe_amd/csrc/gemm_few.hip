@@ -15,15 +15,14 @@
 //         shift and an and-or for every two, and no weight is rounded. sum x
 //         is one more matrix product, with ones, shared by all strips.
 //
-// Design: a wavefront reads its fragments of W straight from memory into
-// registers, several chunks of k ahead; no LDS copy, no barrier inside the k
-// loop. Rows of A behind the expert's count, rows of W behind n and columns
+// Design: rows of W and A go through registers, several steps of k ahead, and
+// through LDS into the products (sum_item). Rows of A behind the expert's count, rows of W behind n and columns
 // behind k are beyond their buffer descriptors' range: those loads return
 // zeros and touch no memory. The strips of all experts form one list that is
-// dealt in equal runs, so experts of any count and calls of any number of
-// experts fill the GPU alike: to wavefronts, each alone with four strips over
-// all of k, where the list is long; to workgroups whose wavefronts split k and
-// add their sums up in LDS, where it is short.
+// dealt to the workgroups in equal runs, so experts of any count and calls of
+// any number of experts fill the GPU alike. Where the list is long, a
+// workgroup's wavefronts take strips beside each other over all of k; where
+// it is short, they split k and add their sums up in LDS.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -40,10 +39,13 @@ constexpr int kFewWaves = 4;      // of a workgroup
 // From this many strips a wavefront (in units of what it holds at once) on,
 // the list is long.
 constexpr int kFewLong = 4;
-// LDS of a workgroup: partial sums, or the wavefronts' rings of scales and
-// the two steps' rows of A.
+// LDS of a workgroup: for each wavefront its rows of W (int4: with its ring
+// of scales behind), then A's; or partial sums.
 constexpr int kRingBytes = 64 * 72;
-constexpr int kPoolBytes = kFewWaves * kRingBytes + 2 * kFewRows * 256;
+constexpr int kPoolWave = 64 * 64 + kRingBytes;
+static_assert(kPoolWave >= 64 * 128);
+constexpr int kPoolA = 32768;
+constexpr int kPoolBytes = kFewWaves * kPoolWave + kPoolA;
 
 __device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
   return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
@@ -83,153 +85,6 @@ __device__ __forceinline__ int strip_rows(const GemmParams& P, const Item& it, i
   if (s >= it.strips) return 0;
   const int left = P.n - 16 * (it.strip + s);
   return left < 16 ? left : 16;
-}
-
-// acc[mf][nf]: bf16 and int4: lane l holds rows 4 (l / 16) + r, r < 4, of
-// column l % 16; fp8: columns 4 (l / 16) + r of row l % 16.
-template <int MF, int NF, bool GATED>
-__device__ __forceinline__ void sum_bf16(const GemmParams& P, const Item& it, int kw, int WK,
-                                         f32x4 (&acc)[MF][NF]) {
-  constexpr int D = MF + NF <= 5 ? 4 : MF + NF <= 6 ? 3 : 2;  // chunks in flight
-  const int lane = threadIdx.x & 63;
-  const uint32_t ld = 2u * (uint32_t)P.k;
-  const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * ld);
-  Rsrc rw[NF];
-  const uint8_t* w = P.w + (uint64_t)it.e * (GATED ? 2 : 1) * P.n * ld;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-    rw[f] = rsrc_of(w + (uint64_t)strip_row<NF, GATED>(P, it.strip, f) * ld,
-                    (uint32_t)strip_rows<NF, GATED>(P, it, f) * ld);
-  const uint32_t row = (lane & 15) * ld, col = 16u * (lane >> 4);
-  const int chunks = (P.k + 63) / 64;
-  v4u wb[D][NF][2], ab[D][MF][2];
-  auto load = [&](int s, int c) {
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-      const uint32_t at = 128u * (uint32_t)c + 64u * j + col;
-      const bool in = c < chunks && at < ld;
-      const uint32_t off = in ? row + at : kOutside;
-#pragma unroll
-      for (int f = 0; f < NF; ++f) wb[s][f][j] = load16(rw[f], off);
-#pragma unroll
-      for (int m = 0; m < MF; ++m) ab[s][m][j] = load16(ra, in ? off + m * 16u * ld : kOutside);
-    }
-  };
-#pragma unroll
-  for (int s = 0; s < D; ++s) load(s, kw + s * WK);
-  for (int c = kw; c < chunks; c += D * WK) {
-#pragma unroll
-    for (int s = 0; s < D; ++s) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j)
-#pragma unroll
-        for (int m = 0; m < MF; ++m)
-#pragma unroll
-          for (int f = 0; f < NF; ++f)
-            acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                __builtin_bit_cast(bf16x8, ab[s][m][j]), __builtin_bit_cast(bf16x8, wb[s][f][j]),
-                acc[m][f], 0, 0, 0);
-      load(s, c + (s + D) * WK);
-      __builtin_amdgcn_sched_barrier(0);  // a stage waits for its own loads, not for the next one's
-    }
-  }
-}
-
-template <int MF, int NF, bool GATED>
-__device__ __forceinline__ void sum_fp8(const GemmParams& P, const Item& it, int kw, int WK,
-                                        f32x4 (&acc)[MF][NF]) {
-  constexpr int D = MF == 4 ? 1 : MF == 2 ? 2 : 3;
-  const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
-  const uint32_t ld = (uint32_t)P.k;
-  const int chunks = P.k / 128;
-  const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * ld);
-  Rsrc rw[NF];
-  const int rows_w = (GATED ? 2 : 1) * P.n, blocks = (rows_w + 127) / 128;
-  const uint8_t* w = P.w + (uint64_t)it.e * rows_w * ld;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-    rw[f] = rsrc_of(w + (uint64_t)strip_row<NF, GATED>(P, it.strip, f) * ld,
-                    (uint32_t)strip_rows<NF, GATED>(P, it, f) * ld);
-  // Scales: lane quarter q loads row fragment q's (lane's row) and strip q's.
-  // Those of a chunk behind k are zeros.
-  const Rsrc rs = rsrc_of(it.a_scales, (uint32_t)it.rows * chunks * 4u);
-  const Rsrc rws = rsrc_of(static_cast<const float*>(P.w_scales) + (uint64_t)it.e * blocks * chunks,
-                           (uint32_t)blocks * chunks * 4u);
-  const uint32_t as_at = 4u * ((MF > 1 ? hi % MF : 0) * 16 + lo) * chunks;
-  const uint32_t ws_at = 4u * (strip_row<NF, GATED>(P, it.strip, hi % NF) / 128) * chunks;
-  const uint32_t row = lo * ld, col = 16u * hi;
-  v4u wb[D][NF][2], ab[D][MF][2];
-  float as[D], sw[D];
-  auto load = [&](int s, int c) {
-    const bool in = c < chunks;
-    const uint32_t off = in ? row + 128u * (uint32_t)c + col : kOutside;
-#pragma unroll
-    for (int j = 0; j < 2; ++j) {
-#pragma unroll
-      for (int f = 0; f < NF; ++f) wb[s][f][j] = load16(rw[f], off + 64u * j);
-#pragma unroll
-      for (int m = 0; m < MF; ++m) ab[s][m][j] = load16(ra, in ? off + 64u * j + m * 16u * ld : kOutside);
-    }
-    as[s] = load_f32(rs, in ? as_at + 4u * c : kOutside);
-    sw[s] = load_f32(rws, in ? ws_at + 4u * c : kOutside);
-  };
-#pragma unroll
-  for (int s = 0; s < D; ++s) load(s, kw + s * WK);
-  for (int c = kw; c < chunks; c += D * WK) {
-#pragma unroll
-    for (int s = 0; s < D; ++s) {
-      f32x4 p[MF][NF];
-#pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        Bf16x16 a[MF];
-#pragma unroll
-        for (int m = 0; m < MF; ++m) a[m] = fp8_to_bf16(ab[s][m][j]);
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const Bf16x16 wv = fp8_to_bf16(wb[s][f][j]);
-#pragma unroll
-          for (int m = 0; m < MF; ++m) {
-            const f32x4 zero = {0, 0, 0, 0};
-            p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv.lo, a[m].lo, j ? p[m][f] : zero, 0, 0, 0);
-            p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv.hi, a[m].hi, p[m][f], 0, 0, 0);
-          }
-        }
-      }
-#pragma unroll
-      for (int m = 0; m < MF; ++m) {
-        const float av = MF > 1 ? __shfl(as[s], m * 16 + lo, 64) : as[s];
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          const float wv = __builtin_bit_cast(
-              float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw[s]), f * 16));
-          const float sc = av * wv;
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[m][f][r] = __builtin_fmaf(sc, p[m][f][r], acc[m][f][r]);
-        }
-      }
-      load(s, c + (s + D) * WK);
-      __builtin_amdgcn_sched_barrier(0);  // a stage waits for its own loads, not for the next one's
-    }
-  }
-}
-
-// Four words of four lane quarters transposed: word j of quarter q becomes
-// word q of quarter j.
-__device__ __forceinline__ void transpose_quarters(uint32_t (&w)[4]) {
-  auto swap32 = [](uint32_t& a, uint32_t& b) {
-    const auto v = __builtin_amdgcn_permlane32_swap(a, b, false, false);
-    a = v[0];
-    b = v[1];
-  };
-  auto swap16 = [](uint32_t& a, uint32_t& b) {
-    const auto v = __builtin_amdgcn_permlane16_swap(a, b, false, false);
-    a = v[0];
-    b = v[1];
-  };
-  swap32(w[0], w[2]);
-  swap32(w[1], w[3]);
-  swap16(w[0], w[1]);
-  swap16(w[2], w[3]);
 }
 
 // A wavefront's int4 scales and zero points. A group's value of 64 weight rows
@@ -307,128 +162,50 @@ struct ScaleRing {
   }
 };
 
-// A chunk is 128 columns: 16 bytes of codes a lane, quarter q the columns
-// [32 q, 32 q + 32). Transposed among the quarters, word j of quarter q holds
-// columns 32 j + 8 q and on: product j covers columns [32 j, 32 j + 32), which
-// lie in one group, and A's fragments are read as they stand.
-template <int MF, int NF, bool GATED, int G>
-__device__ __forceinline__ void sum_int4(const GemmParams& P, const Item& it, int kw, int WK,
-                                         uint8_t* ring_lds, f32x4 (&acc)[MF][NF]) {
-  constexpr int D = MF == 4 ? 1 : MF == 2 ? 2 : 3;
-  constexpr int GROUPS = 128 / G;  // of a chunk
-  const int lane = threadIdx.x & 63;
-  const uint32_t lda = 2u * (uint32_t)P.k, ldw = (uint32_t)P.k / 2;
-  const int groups = P.k / G, chunks = (P.k + 127) / 128;
-  // a run of chunks for each wavefront, for its ring of scales
-  const int c0 = chunks * kw / WK, c1 = chunks * (kw + 1) / WK;
-  const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * lda);
-  Rsrc rw[NF];
-  const int rows_w = (GATED ? 2 : 1) * P.n;
-#pragma unroll
-  for (int f = 0; f < NF; ++f)
-    rw[f] = rsrc_of(P.w + ((uint64_t)it.e * rows_w + strip_row<NF, GATED>(P, it.strip, f)) * ldw,
-                    (uint32_t)strip_rows<NF, GATED>(P, it, f) * ldw);
-  const uint32_t lo = lane & 15, hi = lane >> 4;
-  ScaleRing<NF, GATED> ring;
-  v4u wb[D][NF], ab[D][MF][4];
-  auto load = [&](int s, int c) {
-    const uint32_t wat = 64u * (uint32_t)c + 16u * hi;
-    const uint32_t woff = c < c1 && wat < ldw ? lo * ldw + wat : kOutside;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) wb[s][f] = load16(rw[f], woff);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const uint32_t at = 256u * (uint32_t)c + 64u * j + 16u * hi;
-      const bool in = c < c1 && at < lda;
-#pragma unroll
-      for (int m = 0; m < MF; ++m)
-        ab[s][m][j] = load16(ra, in ? (lo + m * 16u) * lda + at : kOutside);
-    }
-  };
-  const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
-  const CodeMasks masks;
-#pragma unroll
-  for (int s = 0; s < D; ++s) load(s, c0 + s);
-  ring.init(P, it, groups, c0 * GROUPS, ring_lds);
-  for (int c = c0; c < c1; c += D) {
-#pragma unroll
-    for (int s = 0; s < D; ++s) {
-      if (c + s >= c1) break;
-      const f32x4 zero = {0, 0, 0, 0};
-      uint32_t wt[NF][4];
-#pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        wt[f][0] = wb[s][f].x, wt[f][1] = wb[s][f].y, wt[f][2] = wb[s][f].z, wt[f][3] = wb[s][f].w;
-        transpose_quarters(wt[f]);
-      }
-      ring.enter((c + s - c0) * GROUPS);
-#pragma unroll
-      for (int u = 0; u < GROUPS; ++u) {
-        const int g = (c + s) * GROUPS + u;
-        f32x4 p[MF][NF], sum[MF];
-#pragma unroll
-        for (int j = u * (G / 32); j < (u + 1) * (G / 32); ++j) {
-          const bool start = j == u * (G / 32);
-          bf16x8 x[MF];
-#pragma unroll
-          for (int m = 0; m < MF; ++m) {
-            x[m] = a_like_codes(ab[s][m][j]);
-            sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m], ones, start ? zero : sum[m], 0, 0, 0);
-          }
-#pragma unroll
-          for (int f = 0; f < NF; ++f) {
-            const bf16x8 wf = codes_bf16(wt[f][j], masks);
-#pragma unroll
-            for (int m = 0; m < MF; ++m)
-              p[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(x[m], wf, start ? zero : p[m][f], 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int f = 0; f < NF; ++f) {
-          // a group behind k is zeros, times what may be a NaN: scale 0
-          const float read = ring.scale(f, g - c0 * GROUPS);
-          const float sc = g < groups ? read : 0.0f;
-          const float off = ring.zero(f, g - c0 * GROUPS);
-#pragma unroll
-          for (int m = 0; m < MF; ++m)
-#pragma unroll
-            for (int r = 0; r < 4; ++r)
-              acc[m][f][r] = __builtin_fmaf(sc, __builtin_fmaf(-off, sum[m][r], p[m][f][r]), acc[m][f][r]);
-        }
-        __builtin_amdgcn_sched_barrier(0);  // groups in turn: their registers do not add up
-      }
-      load(s, c + s + D);
-    }
-  }
-}
-
-// The long list's form: the four wavefronts of a workgroup take strips beside
-// each other over all of k and share the rows of A through LDS. W still goes
-// straight into registers, D steps ahead; a step's A goes through registers,
-// also D steps ahead (a wait for a load waits for every older one too, so
-// both have to be ordered alike), and is written to LDS as the products read
-// it: as bf16, for int4 in the order of the codes.
 template <int WEIGHT>
 constexpr int step_columns = WEIGHT == kWeightBf16 ? 64 : 128;
+template <int WEIGHT>
+constexpr int step_row_bytes = WEIGHT == kWeightInt4 ? 64 : 128;  // of W
 
-template <int WEIGHT, int G, int MF, int NF, bool GATED>
-__device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, const Item& mine,
-                                           uint8_t* abuf, uint8_t* ring_lds,
-                                           f32x4 (&acc)[MF][NF]) {
+// The sums of one item: acc[m][f], bf16 and int4: lane l holds rows 4 (l / 16)
+// + r, r < 4, of column l % 16; fp8: columns 4 (l / 16) + r of row l % 16.
+//
+// A step is 128 bytes of every row of W (int4: 64) and the columns of A that
+// belong to it. Both go through registers, D steps ahead, and from there
+// through LDS. Memory is read whole lines at a time, eight lanes a line:
+// fragments read in place, 16 rows of 16 bytes at once, cost the vector cache
+// an access a lane, and that and not memory bounded the kernel (128-token
+// decode: fp8 1377 us, 4-bit 860). W's part of LDS is the wavefront's own: no
+// barrier. A is as the products read it: bf16, for int4 in the codes' order.
+// SPLIT: a wavefront has a run of the steps and its own part for A; else the
+// four share A in two buffers, with a barrier a step. A wait for a load waits
+// for every older one too, so A's and W's loads are ordered as they are used.
+template <int WEIGHT, int G, int MF, int NF, bool GATED, bool SPLIT>
+__device__ __forceinline__ void sum_item(const GemmParams& P, const Item& it, const Item& mine,
+                                         uint8_t* pool, f32x4 (&acc)[MF][NF]) {
   constexpr bool FP8 = WEIGHT == kWeightFp8, INT4 = WEIGHT == kWeightInt4;
   constexpr int KS = step_columns<WEIGHT>;
-  constexpr int ROW = 2 * KS;                       // LDS bytes of a row of a step
+  constexpr int ROW = 2 * KS, CH = ROW / 16;        // LDS bytes and 16-byte chunks of a row of A
+  constexpr int WROW = step_row_bytes<WEIGHT>, WCH = WROW / 16;
   constexpr int STEP = MF * 16 * ROW;
-  constexpr int CH = ROW / 16;                      // 16-byte chunks of it
-  constexpr int D = MF == 4 ? 2 : 3;
   constexpr int A_ITEM = FP8 ? 1 : 2;               // bytes of a value of A in memory
   constexpr int A_CH = KS * A_ITEM / 16;            // 16-byte loads of a row
-  constexpr int AL = (MF * 16 * A_CH + 255) / 256;  // loads of a thread
-  constexpr int WL = KS * (FP8 ? 2 : INT4 ? 1 : 4) / 128;  // 16-byte loads of a strip
-  constexpr int GROUPS = INT4 ? 128 / G : 1;
-  const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
-  const int steps = (P.k + KS - 1) / KS;
+  constexpr int T = SPLIT ? 64 : kFewWaves * 64;    // threads that bring A in
+  constexpr int AL = (MF * 16 * A_CH + T - 1) / T;  // loads of each
+  constexpr int WL = WCH / 4;                       // loads of a strip
+  constexpr int GROUPS = INT4 ? KS / G : 1;
+  constexpr int FB = MF == 4 ? 1 : NF;              // fp8, int4: strips at a time
+  constexpr int ROOM = (INT4 ? 120 : FP8 ? 160 : 176) - 4 * MF * NF - (WEIGHT == kWeightBf16 ? 0 : 4 * MF * FB);
+  constexpr int FITS = ROOM / (4 * (NF * WL + AL));
+  constexpr int D = FITS < 2 ? 2 : FITS > 4 ? 4 : FITS;
+  static_assert(kFewWaves * STEP <= kPoolA || (!SPLIT && 2 * STEP <= kPoolA));
+  const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int tid = SPLIT ? lane : threadIdx.x;
+  uint8_t* wlds = pool + wave * kPoolWave;
+  uint8_t* alds = pool + kFewWaves * kPoolWave + (SPLIT ? wave * STEP : 0);
+  const int all = (P.k + KS - 1) / KS;
+  const int s0 = SPLIT ? all * wave / kFewWaves : 0, s1 = SPLIT ? all * (wave + 1) / kFewWaves : all;
   const uint32_t lda = (uint32_t)P.k * A_ITEM;
   const uint32_t ldw = INT4 ? (uint32_t)P.k / 2 : lda;
   const Rsrc ra = rsrc_of(it.a, (uint32_t)it.rows * lda);
@@ -441,7 +218,7 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
 
   // Scales. fp8: lane quarter q loads row fragment q's and strip q's; those
   // behind k are zeros. int4: a ring.
-  const int groups = INT4 ? P.k / G : steps, blocks = (rows_w + 127) / 128;
+  const int groups = INT4 ? P.k / G : all, blocks = (rows_w + 127) / 128;
   const Rsrc rs = rsrc_of(static_cast<const float*>(P.w_scales) + (FP8 ? (uint64_t)it.e * blocks * groups : 0),
                           FP8 ? 4u * blocks * groups : 0u);
   const Rsrc ras = rsrc_of(it.a_scales, FP8 ? (uint32_t)it.rows * groups * 4u : 0u);
@@ -454,18 +231,18 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
   auto load_a = [&](int s, int step) {
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
-      const int q = tid + 256 * i, row = q / A_CH;
+      const int q = tid + T * i, row = q / A_CH;
       const uint32_t at = (uint32_t)step * (KS * A_ITEM) + 16u * (q % A_CH);
-      const bool in = step < steps && at < lda && row < MF * 16;
+      const bool in = step < s1 && at < lda && row < MF * 16;
       ab[s][i] = load16(ra, in ? (uint32_t)row * lda + at : kOutside);
     }
   };
   auto store_a = [&](int s, int step) {
-    uint8_t* to = abuf + (step & 1) * STEP;
+    uint8_t* to = alds + (SPLIT ? 0 : (step & 1) * STEP);
 #pragma unroll
     for (int i = 0; i < AL; ++i) {
-      const int q = tid + 256 * i, row = q / A_CH, c = q % A_CH;
-      if (MF * 16 * A_CH % 256 && row >= MF * 16) break;
+      const int q = tid + T * i, row = q / A_CH, c = q % A_CH;
+      if (MF * 16 * A_CH % T && row >= MF * 16) break;
       uint8_t* r = to + row * ROW;
       if constexpr (FP8) {
         const Bf16x16 v = fp8_to_bf16(ab[s][i]);
@@ -478,53 +255,69 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
       }
     }
   };
+  const int wr = lane / WCH, wc = lane % WCH;  // this lane's row and chunk of a load of W
+  auto w_swap = [](int row) { return INT4 ? row >> 2 : row; };
   auto load_w = [&](int s, int step) {
+    const uint32_t at = (uint32_t)step * WROW + 16u * wc;
+    const uint32_t off = step < s1 && at < ldw ? wr * ldw + at : kOutside;
 #pragma unroll
-    for (int j = 0; j < WL; ++j) {
-      const uint32_t at = (uint32_t)step * (64 * WL) + 64u * j + 16u * hi;
-      const uint32_t off = step < steps && at < ldw ? lo * ldw + at : kOutside;
+    for (int i = 0; i < WL; ++i)
 #pragma unroll
-      for (int f = 0; f < NF; ++f) wb[s][f][j] = load16(rw[f], off);
-    }
+      for (int f = 0; f < NF; ++f) wb[s][f][i] = load16(rw[f], off + i * (64 / WCH) * ldw);
     if constexpr (FP8) {
-      as[s] = load_f32(ras, step < steps ? as_at + 4u * step : kOutside);
-      sw[s] = load_f32(rs, step < steps ? s_at + 4u * step : kOutside);
+      as[s] = load_f32(ras, step < s1 ? as_at + 4u * step : kOutside);
+      sw[s] = load_f32(rs, step < s1 ? s_at + 4u * step : kOutside);
     }
+  };
+  auto store_w = [&](int s) {
+#pragma unroll
+    for (int f = 0; f < NF; ++f)
+#pragma unroll
+      for (int i = 0; i < WL; ++i) {
+        const int row = i * (64 / WCH) + wr;
+        *reinterpret_cast<v4u*>(wlds + (f * 16 + row) * WROW + ((wc ^ w_swap(row)) & (WCH - 1)) * 16) =
+            wb[s][f][i];
+      }
   };
   const v4u one = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
   const bf16x8 ones = __builtin_bit_cast(bf16x8, one);
   const CodeMasks masks;
   const f32x4 zero = {0, 0, 0, 0};
-  auto multiply = [&](int s, int step) __attribute__((always_inline)) {
-    const uint8_t* from = abuf + (step & 1) * STEP;
+  auto multiply = [&](float as_s, float sw_s, int step) __attribute__((always_inline)) {
+    const uint8_t* from = alds + (SPLIT ? 0 : (step & 1) * STEP);
     auto a_chunk = [&](int m, int c) {
       const int row = m * 16 + lo;
       return *reinterpret_cast<const bf16x8*>(from + row * ROW + ((c ^ row) & (CH - 1)) * 16);
     };
+    auto w_chunk = [&](int f, int c) {
+      return *reinterpret_cast<const v4u*>(wlds + (f * 16 + lo) * WROW + ((c ^ w_swap(lo)) & (WCH - 1)) * 16);
+    };
     if constexpr (WEIGHT == kWeightBf16) {
 #pragma unroll
-      for (int j = 0; j < WL; ++j)
+      for (int j = 0; j < 2; ++j) {
+        bf16x8 w[NF];
+#pragma unroll
+        for (int f = 0; f < NF; ++f) w[f] = __builtin_bit_cast(bf16x8, w_chunk(f, 4 * j + hi));
 #pragma unroll
         for (int m = 0; m < MF; ++m) {
           const bf16x8 a = a_chunk(m, 4 * j + hi);
 #pragma unroll
           for (int f = 0; f < NF; ++f)
-            acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                a, __builtin_bit_cast(bf16x8, wb[s][f][j]), acc[m][f], 0, 0, 0);
+            acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, w[f], acc[m][f], 0, 0, 0);
         }
+      }
     } else if constexpr (FP8) {
       float av[MF];
 #pragma unroll
-      for (int m = 0; m < MF; ++m) av[m] = MF > 1 ? __shfl(as[s], m * 16 + lo, 64) : as[s];
-      constexpr int FB = MF == 4 ? 1 : NF;  // strips at a time
+      for (int m = 0; m < MF; ++m) av[m] = MF > 1 ? __shfl(as_s, m * 16 + lo, 64) : as_s;
 #pragma unroll
       for (int f0 = 0; f0 < NF; f0 += FB) {
         f32x4 p[MF][FB];
 #pragma unroll
-        for (int j = 0; j < WL; ++j) {
+        for (int j = 0; j < 2; ++j) {
           Bf16x16 w[FB];
 #pragma unroll
-          for (int f = 0; f < FB; ++f) w[f] = fp8_to_bf16(wb[s][f0 + f][j]);
+          for (int f = 0; f < FB; ++f) w[f] = fp8_to_bf16(w_chunk(f0 + f, 4 * j + hi));
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
             const bf16x8 a0 = a_chunk(m, 8 * j + 2 * hi), a1 = a_chunk(m, 8 * j + 2 * hi + 1);
@@ -538,7 +331,7 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
 #pragma unroll
         for (int f = 0; f < FB; ++f) {
           const float wv = __builtin_bit_cast(
-              float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw[s]), (f0 + f) * 16));
+              float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, sw_s), (f0 + f) * 16));
 #pragma unroll
           for (int m = 0; m < MF; ++m) {
             const float sc = av[m] * wv;
@@ -550,19 +343,20 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
         if (FB < NF) __builtin_amdgcn_sched_barrier(0);  // strips in turn, for the registers
       }
     } else {
-      // Groups of 128: the word j of quarter q holds columns 32 q + 8 j and on,
-      // and A is read to match. Smaller groups: transposed, see sum_int4.
-      ring.enter(step * GROUPS);
+      // Product j of a strip covers columns [32 j, 32 j + 32) of the step,
+      // which lie in one group: lane quarter q holds 8 of them, word q of
+      // chunk j.
+      ring.enter((step - s0) * GROUPS);
       uint32_t wt[NF][4];
 #pragma unroll
-      for (int f = 0; f < NF; ++f) {
-        wt[f][0] = wb[s][f][0].x, wt[f][1] = wb[s][f][0].y, wt[f][2] = wb[s][f][0].z, wt[f][3] = wb[s][f][0].w;
-        if constexpr (G < 128) transpose_quarters(wt[f]);
-      }
+      for (int f = 0; f < NF; ++f)
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          wt[f][j] = *reinterpret_cast<const uint32_t*>(
+              wlds + (f * 16 + lo) * WROW + ((j ^ w_swap(lo)) & (WCH - 1)) * 16 + 4 * hi);
 #pragma unroll
       for (int u = 0; u < GROUPS; ++u) {
-        const int g = step * GROUPS + u;
-        constexpr int FB = MF == 4 ? 1 : NF;
+        const int g = step * GROUPS + u, gr = g - s0 * GROUPS;
         f32x4 sum[MF];
 #pragma unroll
         for (int f0 = 0; f0 < NF; f0 += FB) {
@@ -575,7 +369,7 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
             for (int f = 0; f < FB; ++f) w[f] = codes_bf16(wt[f0 + f][j], masks);
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
-              const bf16x8 a = a_chunk(m, G < 128 ? 4 * j + hi : 4 * hi + j);
+              const bf16x8 a = a_chunk(m, 4 * j + hi);
               if (f0 == 0)
                 sum[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, ones, start ? zero : sum[m], 0, 0, 0);
 #pragma unroll
@@ -586,9 +380,9 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
 #pragma unroll
           for (int f = 0; f < FB; ++f) {
             // a group behind k is zeros, times what may be a NaN: scale 0
-            const float read = ring.scale(f0 + f, g);
+            const float read = ring.scale(f0 + f, gr);
             const float sc = G == 128 || g < groups ? read : 0.0f;
-            const float off = ring.zero(f0 + f, g);
+            const float off = ring.zero(f0 + f, gr);
 #pragma unroll
             for (int m = 0; m < MF; ++m)
 #pragma unroll
@@ -603,26 +397,35 @@ __device__ __forceinline__ void sum_shared(const GemmParams& P, const Item& it, 
     }
   };
 
-  // ab[i] holds step i's rows of A (mod D), wb[i] its weights
 #pragma unroll
   for (int s = 0; s < D; ++s) {
-    load_a(s, s);
-    load_w(s, s);
+    load_a(s, s0 + s);
+    load_w(s, s0 + s);
   }
-  if constexpr (INT4) ring.init(P, mine, groups, 0, ring_lds);
-  __syncthreads();  // the buffers' last reader is done
-  store_a(0, 0);
-  load_a(0, D);
-  for (int k = 0; k < steps; k += D) {
+  if constexpr (INT4) ring.init(P, mine, groups, s0 * GROUPS, wlds + kPoolWave - kRingBytes);
+  if constexpr (!SPLIT) {
+    __syncthreads();  // the buffers' last reader is done
+    store_a(0, 0);
+    load_a(0, D);
+  }
+  for (int k = s0; k < s1; k += D) {
 #pragma unroll
     for (int s = 0; s < D; ++s) {
       const int step = k + s;
-      if (step >= steps) break;  // the same for the whole workgroup
-      __syncthreads();           // step's A is there, and the step before is read
-      store_a((s + 1) % D, step + 1);
-      load_a((s + 1) % D, step + 1 + D);
-      multiply(s, step);
+      if (step >= s1) break;  // the same for all who share A
+      if constexpr (SPLIT) {
+        store_a(s, step);
+        load_a(s, step + D);
+      } else {
+        __syncthreads();  // step's A is there, and the step before is read
+        store_a((s + 1) % D, step + 1);
+        load_a((s + 1) % D, step + 1 + D);
+      }
+      store_w(s);
+      const float as_s = FP8 ? as[s] : 0.0f, sw_s = FP8 ? sw[s] : 0.0f;
       load_w(s, step + D);
+      multiply(as_s, sw_s, step);
+      __builtin_amdgcn_sched_barrier(0);  // a step waits for its own loads, not for the next one's
     }
   }
 }
@@ -657,15 +460,7 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, uin
   for (int m = 0; m < MF; ++m)
 #pragma unroll
     for (int f = 0; f < NF; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-  uint8_t* ring = pool + wave * kRingBytes;
-  if constexpr (!SPLIT)
-    sum_shared<WEIGHT, G, MF, NF, GATED>(P, it, mine, pool + kFewWaves * kRingBytes, ring, acc);
-  else if constexpr (WEIGHT == kWeightBf16)
-    sum_bf16<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
-  else if constexpr (WEIGHT == kWeightFp8)
-    sum_fp8<MF, NF, GATED>(P, mine, wave, kFewWaves, acc);
-  else
-    sum_int4<MF, NF, GATED, G>(P, mine, wave, kFewWaves, ring, acc);
+  sum_item<WEIGHT, G, MF, NF, GATED, SPLIT>(P, it, mine, pool, acc);
 
   auto meet = [] {
     if constexpr (ALONE) {
@@ -675,8 +470,7 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, uin
       __syncthreads();
     }
   };
-  // the pool was the rings' and A's until here
-  if (!SPLIT || WEIGHT == kWeightInt4) __syncthreads();
+  __syncthreads();  // the pool was W's and A's until here
   const int lo = lane & 15, hi = lane >> 4;
   constexpr int WAVE = MP * 16 * LD;
   float* part = reinterpret_cast<float*>(pool);
@@ -739,8 +533,7 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, uin
     }
     meet();
   }
-  // before the next item's rings: a wavefront's part of the pool was not
-  // where its ring is
+  // before the next item: a wavefront's outputs were not where its rows are
   if (ALONE) __syncthreads();
 }
 
@@ -750,15 +543,16 @@ __device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it
     do_item<WEIGHT, G, 1, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
   } else if (it.rows <= 32) {
     do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
-  } else if constexpr (SPLIT && WEIGHT != kWeightBf16 && NF == 4) {
-    // registers hold 64 rows of A beside two strips
-    constexpr int SF = GATED ? 1 : 2;
+  } else if constexpr (SPLIT && WEIGHT != kWeightBf16) {
+    // each wavefront's own 32 rows of A are what LDS holds
     Item half = it;
-    half.strips = it.strips < SF ? it.strips : SF;
-    do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, pool);
-    half.strip += SF;
-    half.strips = it.strips - SF;
-    if (half.strips > 0) do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, pool);
+    half.rows = 32;
+    do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, half, pool);
+    half.rows = it.rows - 32;
+    half.row0 += 32;
+    half.a += 32 * (uint64_t)P.k * (WEIGHT == kWeightFp8 ? 1 : 2);
+    if (WEIGHT == kWeightFp8) half.a_scales += 32 * (uint64_t)(P.k / 128);
+    do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, half, pool);
   } else {
     do_item<WEIGHT, G, 4, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
   }
