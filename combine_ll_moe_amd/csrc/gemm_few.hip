@@ -54,6 +54,14 @@ __device__ __forceinline__ v4u load16(Rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, 0);
 }
 
+// The lane, opaque to the compiler: it would keep every form's LDS addresses
+// in registers across all items.
+__device__ __forceinline__ int opaque_lane() {
+  int lane = threadIdx.x & 63;
+  asm volatile("" : "+v"(lane));
+  return lane;
+}
+
 __device__ __forceinline__ float load_f32(Rsrc r, uint32_t off) {
   return __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(r, (int)off, 0, 0));
 }
@@ -105,11 +113,13 @@ struct ScaleRing {
   uint32_t at[NF], zat[NF];     // LDS: row f * 16 + lane % 16
   uint32_t phase[NF], zphase[NF];
   float none;
+  int lane;
   static_assert(kBytes <= kRingBytes);
 
   __device__ __forceinline__ void init(const GemmParams& P, const Item& it, int groups, int first,
-                                       uint8_t* ring) {
-    const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
+                                       uint8_t* ring, int lane_) {
+    lane = lane_;
+    const int lo = lane & 15, hi = lane >> 4;
     const int rows_w = (GATED ? 2 : 1) * P.n;
     const uint32_t values = (uint32_t)rows_w * groups;
     rs = rsrc_of(static_cast<const uint16_t*>(P.w_scales) + (uint64_t)it.e * values, 2 * values);
@@ -141,7 +151,6 @@ struct ScaleRing {
     zblock += 8;
   }
   __device__ __forceinline__ void put(int slot) {
-    const int lane = threadIdx.x & 63;
     *reinterpret_cast<v4u*>(lds + lane * kRow + slot * 16) = next;
     *reinterpret_cast<v2u*>(lds + 64 * kRow + lane * kZeroRow + slot * 8) = znext;
   }
@@ -194,14 +203,14 @@ __device__ __forceinline__ void sum_item(const GemmParams& P, const Item& it, co
   constexpr int AL = (MF * 16 * A_CH + T - 1) / T;  // loads of each
   constexpr int WL = WCH / 4;                       // loads of a strip
   constexpr int GROUPS = INT4 ? KS / G : 1;
-  constexpr int FB = MF == 4 ? 1 : NF;              // fp8, int4: strips at a time
-  constexpr int ROOM = (INT4 ? 120 : FP8 ? 160 : 176) - 4 * MF * NF - (WEIGHT == kWeightBf16 ? 0 : 4 * MF * FB);
+  constexpr int FB = MF == 4 ? 1 : INT4 && MF == 2 && NF == 4 ? 2 : NF;  // fp8, int4: strips at a time
+  constexpr int ROOM = (INT4 ? 120 : FP8 || SPLIT ? 160 : 176) - 4 * MF * NF - (WEIGHT == kWeightBf16 ? 0 : 4 * MF * FB);
   constexpr int FITS = ROOM / (4 * (NF * WL + AL));
   constexpr int D = FITS < 2 ? 2 : FITS > 4 ? 4 : FITS;
   static_assert(kFewWaves * STEP <= kPoolA || (!SPLIT && 2 * STEP <= kPoolA));
-  const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
+  const int lane = opaque_lane(), lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tid = SPLIT ? lane : threadIdx.x;
+  const int tid = SPLIT ? lane : wave * 64 + lane;
   uint8_t* wlds = pool + wave * kPoolWave;
   uint8_t* alds = pool + kFewWaves * kPoolWave + (SPLIT ? wave * STEP : 0);
   const int all = (P.k + KS - 1) / KS;
@@ -347,13 +356,10 @@ __device__ __forceinline__ void sum_item(const GemmParams& P, const Item& it, co
       // which lie in one group: lane quarter q holds 8 of them, word q of
       // chunk j.
       ring.enter((step - s0) * GROUPS);
-      uint32_t wt[NF][4];
-#pragma unroll
-      for (int f = 0; f < NF; ++f)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-          wt[f][j] = *reinterpret_cast<const uint32_t*>(
-              wlds + (f * 16 + lo) * WROW + ((j ^ w_swap(lo)) & (WCH - 1)) * 16 + 4 * hi);
+      auto w_word = [&](int f, int j) {
+        return *reinterpret_cast<const uint32_t*>(
+            wlds + (f * 16 + lo) * WROW + ((j ^ w_swap(lo)) & (WCH - 1)) * 16 + 4 * hi);
+      };
 #pragma unroll
       for (int u = 0; u < GROUPS; ++u) {
         const int g = step * GROUPS + u, gr = g - s0 * GROUPS;
@@ -366,7 +372,7 @@ __device__ __forceinline__ void sum_item(const GemmParams& P, const Item& it, co
             const bool start = j == u * (G / 32);
             bf16x8 w[FB];
 #pragma unroll
-            for (int f = 0; f < FB; ++f) w[f] = codes_bf16(wt[f0 + f][j], masks);
+            for (int f = 0; f < FB; ++f) w[f] = codes_bf16(w_word(f0 + f, j), masks);
 #pragma unroll
             for (int m = 0; m < MF; ++m) {
               const bf16x8 a = a_chunk(m, 4 * j + hi);
@@ -402,7 +408,7 @@ __device__ __forceinline__ void sum_item(const GemmParams& P, const Item& it, co
     load_a(s, s0 + s);
     load_w(s, s0 + s);
   }
-  if constexpr (INT4) ring.init(P, mine, groups, s0 * GROUPS, wlds + kPoolWave - kRingBytes);
+  if constexpr (INT4) ring.init(P, mine, groups, s0 * GROUPS, wlds + kPoolWave - kRingBytes, lane);
   if constexpr (!SPLIT) {
     __syncthreads();  // the buffers' last reader is done
     store_a(0, 0);
@@ -446,9 +452,9 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, uin
   constexpr int FIT = kPoolBytes / (kFewWaves * 16 * LD * 4);
   constexpr int MP = FIT >= MF ? MF : FIT >= 2 ? 2 : 1;
   static_assert(FIT >= 1);
-  const int lane = threadIdx.x & 63;
+  const int lane = opaque_lane();
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int tid = ALONE ? lane : threadIdx.x;
+  const int tid = ALONE ? lane : wave * 64 + lane;
   Item mine = it;
   if constexpr (!SPLIT) {
     const int s0 = it.strips * wave / kFewWaves;
@@ -553,6 +559,15 @@ __device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it
     half.a += 32 * (uint64_t)P.k * (WEIGHT == kWeightFp8 ? 1 : 2);
     if (WEIGHT == kWeightFp8) half.a_scales += 32 * (uint64_t)(P.k / 128);
     do_item<WEIGHT, G, 2, NF, GATED, OUT_FP8, SPLIT>(P, half, pool);
+  } else if constexpr (SPLIT && NF == 4) {
+    // registers hold 64 rows of A beside two strips
+    constexpr int SF = GATED ? 1 : 2;
+    Item half = it;
+    half.strips = it.strips < SF ? it.strips : SF;
+    do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, pool);
+    half.strip += SF;
+    half.strips = it.strips - SF;
+    if (half.strips > 0) do_item<WEIGHT, G, 4, NF / 2, GATED, OUT_FP8, SPLIT>(P, half, pool);
   } else {
     do_item<WEIGHT, G, 4, NF, GATED, OUT_FP8, SPLIT>(P, it, pool);
   }
