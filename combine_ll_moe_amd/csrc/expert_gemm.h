@@ -49,11 +49,27 @@ constexpr int kTileRows = 256;
 __host__ __device__ __forceinline__ int few_first(int rows, int most) {
   return rows <= most ? 0 : rows - rows % kTileRows;
 }
-__host__ __device__ __forceinline__ int few_tiles(int rows, int most) {
+__host__ __device__ __forceinline__ int few_rows(int rows, int most) {
   if (rows <= 0) return 0;
-  if (rows <= most) return (rows - 1) / kFewRows + 1;
+  if (rows <= most) return rows;
   const int left = rows % kTileRows;
-  return left > 0 && left <= kFewRows;
+  return left <= kFewRows ? left : 0;
+}
+// What a strip of W costs the few kernel with a tile of so many rows, in
+// eighths of one with up to 16 (measured, us for 64 experts of 2048 x 7168
+// weights at 16, 32 and 64 rows: bf16 314, 314, 331; fp8 169, 183, 203; int4
+// 107, 140, 210).
+template <int WEIGHT>
+__device__ __forceinline__ int strip_cost(int rows) {
+  if (WEIGHT == kWeightBf16) return rows <= 32 ? 8 : 9;
+  if (WEIGHT == kWeightFp8) return rows <= 16 ? 8 : rows <= 32 ? 9 : 10;
+  return rows <= 16 ? 8 : rows <= 32 ? 10 : 16;
+}
+// The same of all row tiles of few_rows rows.
+template <int WEIGHT>
+__device__ __forceinline__ int tiles_cost(int rows) {
+  const int whole = rows / kFewRows, left = rows % kFewRows;
+  return whole * strip_cost<WEIGHT>(kFewRows) + (left ? strip_cost<WEIGHT>(left) : 0);
 }
 __host__ __device__ __forceinline__ int big_tiles(int rows, int most) {
   return rows <= most ? 0 : rows / kTileRows + (rows % kTileRows > kFewRows);
@@ -75,12 +91,12 @@ __device__ __forceinline__ uint32_t wave_sums(uint32_t v) {
   return dpp_add<0x143, 0xC, 0xF>(v);  // row_bcast:31
 }
 
-// Row tiles before each expert: pre[e], e <= E, of the few kernel or of the
-// tile kernel; the rows of each expert behind them. All THREADS threads call
-// it; scan: one word a wavefront.
-template <int THREADS, bool FEW>
-__device__ __forceinline__ void tile_prefix(const GemmParams& P, int most, uint32_t* pre,
-                                            uint32_t* scan) {
+// What stands before each expert: pre[e], e <= E, of measure(rows), such as
+// its row tiles; the rows of each expert behind them. All THREADS threads
+// call it; scan: one word a wavefront.
+template <int THREADS, class Measure>
+__device__ __forceinline__ void tile_prefix(const GemmParams& P, uint32_t* pre, uint32_t* scan,
+                                            Measure measure) {
   const int tid = threadIdx.x, lane = tid & 63, E = P.num_experts;
   const int run = (E + THREADS - 1) / THREADS;
   const int e0 = tid * run < E ? tid * run : E, e1 = e0 + run < E ? e0 + run : E;
@@ -88,7 +104,7 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, int most, uint3
   for (int e = e0; e < e1; ++e) {
     int c = P.counts[e];
     c = c < P.max_tokens ? c : P.max_tokens;
-    const uint32_t t = (uint32_t)(FEW ? few_tiles(c, most) : big_tiles(c, most));
+    const uint32_t t = (uint32_t)measure(c);
     pre[e] = sum;
     pre[E + 1 + e] = (uint32_t)c;
     sum += t;
@@ -190,7 +206,7 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float p0, float p1, float p2, flo
   return ((uint32_t)w & ~m) | (0x7F7F7F7Fu & m);
 }
 
-// Each takes its rows of every expert (few_tiles, big_tiles).
+// Each takes its rows of every expert (few_rows, big_tiles).
 hipError_t launch_gemm_few(const GemmParams& p, int most, hipStream_t stream);
 hipError_t launch_gemm_tile(const GemmParams& p, int most, hipStream_t stream);
 

@@ -108,8 +108,8 @@ struct ScaleRing {
   Rsrc rs, rz;
   uint8_t* lds;
   uint32_t block, zblock;       // this lane's next block's offset
-  v4u next;
-  v2u znext;
+  v4u next, head[2];
+  v2u znext, zhead[2];
   uint32_t at[NF], zat[NF];     // LDS: row f * 16 + lane % 16
   uint32_t phase[NF], zphase[NF];
   float none;
@@ -138,11 +138,16 @@ struct ScaleRing {
       phase[f] = 2 * g & 15;
       zphase[f] = g & 7;
     }
+    // three blocks at once: the first two to LDS, when `settle` is called
     fetch();
-    put(0);
+    head[0] = next, zhead[0] = znext;
     fetch();
-    put(1);
+    head[1] = next, zhead[1] = znext;
     fetch();
+  }
+  __device__ __forceinline__ void settle() {
+    put(0, head[0], zhead[0]);
+    put(1, head[1], zhead[1]);
   }
   __device__ __forceinline__ void fetch() {
     next = load16(rs, block);
@@ -150,15 +155,15 @@ struct ScaleRing {
     block += 16;
     zblock += 8;
   }
-  __device__ __forceinline__ void put(int slot) {
-    *reinterpret_cast<v4u*>(lds + lane * kRow + slot * 16) = next;
-    *reinterpret_cast<v2u*>(lds + 64 * kRow + lane * kZeroRow + slot * 8) = znext;
+  __device__ __forceinline__ void put(int slot, v4u v, v2u z) {
+    *reinterpret_cast<v4u*>(lds + lane * kRow + slot * 16) = v;
+    *reinterpret_cast<v2u*>(lds + 64 * kRow + lane * kZeroRow + slot * 8) = z;
   }
   // Before group g (from `first`) is read: at a window's start the block
   // behind it comes in, in the place of the one before it.
   __device__ __forceinline__ void enter(int g) {
     if (g > 0 && g % 8 == 0) {
-      put((g / 8 + 1) & 1);
+      put((g / 8 + 1) & 1, next, znext);
       fetch();
     }
   }
@@ -403,12 +408,13 @@ __device__ __forceinline__ void sum_item(const GemmParams& P, const Item& it, co
     }
   };
 
+  if constexpr (INT4) ring.init(P, mine, groups, s0 * GROUPS, wlds + kPoolWave - kRingBytes, lane);
 #pragma unroll
   for (int s = 0; s < D; ++s) {
     load_a(s, s0 + s);
     load_w(s, s0 + s);
   }
-  if constexpr (INT4) ring.init(P, mine, groups, s0 * GROUPS, wlds + kPoolWave - kRingBytes, lane);
+  if constexpr (INT4) ring.settle();
   if constexpr (!SPLIT) {
     __syncthreads();  // the buffers' last reader is done
     store_a(0, 0);
@@ -573,58 +579,57 @@ __device__ __forceinline__ void do_item_rows(const GemmParams& P, const Item& it
   }
 }
 
-// The units [u0, u1) of a list of `tiles` x `units`. A unit is an output
-// strip, or (fp8 out, where a row's 128 columns share a scale) 128 columns.
+// The run [u0, u1) of the list. A tile of rows is `units` units long, each of
+// strip_cost: a unit is an output strip, or (fp8 out, where a row's 128 columns
+// share a scale) 128 columns. Whose first place lies in the run is the run's.
 template <int WEIGHT, int G, bool GATED, bool OUT_FP8, bool SPLIT>
 __device__ __forceinline__ void do_run(const GemmParams& P, int most, const uint32_t* pre,
                                        uint8_t* pool, int units, uint64_t u0, uint64_t u1) {
   constexpr int SF = GATED ? kFewFrags / 2 : kFewFrags;
-  if (u0 >= u1) return;
-  // division in 32 bits wherever the list allows it
-  uint32_t tile = u1 >> 32 ? (uint32_t)(u0 / (uint32_t)units) : (uint32_t)u0 / (uint32_t)units;
-  int unit = (int)(u0 - (uint64_t)tile * units);
-  int e = expert_of_tile(pre, P.num_experts, tile);
-  uint32_t end = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e + 1]);
-  for (uint64_t left = u1 - u0; left > 0;) {
-    if (unit == units) {
-      unit = 0;
-      if (++tile == end) {
-        e = expert_of_tile(pre, P.num_experts, tile);
-        end = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e + 1]);
-      }
-    }
-    const int t = (int)(tile - (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e]));
+  const uint32_t full = (uint32_t)units * strip_cost<WEIGHT>(kFewRows);  // places of a whole tile
+  for (uint64_t u = u0; u < u1;) {
+    // division in 32 bits wherever the list allows it
+    const uint32_t at = u1 >> 32 ? (uint32_t)(u / (uint32_t)units) : (uint32_t)u / (uint32_t)units;
+    const int e = expert_of_tile(pre, P.num_experts, at);
     const int c = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + e]);
+    const uint64_t first = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e]) * units;
+    const uint32_t in_e = (uint32_t)(u - first);
+    const int t = (int)(in_e / full);
+    const int row = few_first(c, most) + t * kFewRows;
     Item it;
     it.e = e;
-    const int first = few_first(c, most) + t * kFewRows;
-    it.row0 = (int64_t)e * P.max_tokens + first;
-    it.rows = c - first < kFewRows ? c - first : kFewRows;
+    it.row0 = (int64_t)e * P.max_tokens + row;
+    it.rows = c - row < kFewRows ? c - row : kFewRows;
     it.a = P.a + (uint64_t)it.row0 * P.k * (WEIGHT == kWeightFp8 ? 1 : 2);
     it.a_scales = WEIGHT == kWeightFp8 ? P.a_scales + (uint64_t)it.row0 * (P.k / 128) : nullptr;
-    int here = units - unit;
-    here = left < (uint64_t)here ? (int)left : here;
-    int done = 1;
-    it.strip = unit;
-    if constexpr (OUT_FP8) {
-      it.strip = unit * 8;
-      it.strips = 8;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, pool);
-    } else if constexpr (!SPLIT) {
-      // as many strips as the workgroup holds, in items of like size
-      const int items = (here + kFewWaves * SF - 1) / (kFewWaves * SF);
-      it.strips = done = (here + items - 1) / items;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, pool);
-    } else if (here >= SF) {
-      it.strips = done = SF;
-      do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, true>(P, it, pool);
-    } else {
-      // the run's last strips, fewer than a wavefront holds
+    const uint32_t cost = (uint32_t)strip_cost<WEIGHT>(it.rows);
+    const uint64_t base = first + (uint64_t)t * full;
+    int unit = (int)(((uint32_t)(u - base) + cost - 1) / cost);
+    const uint64_t tile_end = base + (uint64_t)units * cost;
+    const int end = u1 < tile_end ? (int)(((uint32_t)(u1 - base) + cost - 1) / cost) : units;
+    while (unit < end) {
+      int done = 1;
+      it.strip = unit;
       it.strips = 1;
-      do_item_rows<WEIGHT, G, GATED ? 2 : 1, GATED, OUT_FP8, true>(P, it, pool);
+      if constexpr (OUT_FP8) {
+        it.strip = unit * 8;
+        it.strips = 8;
+        do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, pool);
+      } else if constexpr (!SPLIT) {
+        // as many strips as the workgroup holds, in items of like size
+        const int items = (end - unit + kFewWaves * SF - 1) / (kFewWaves * SF);
+        it.strips = done = (end - unit + items - 1) / items;
+        do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, false>(P, it, pool);
+      } else if (end - unit >= SF) {
+        it.strips = done = SF;
+        do_item_rows<WEIGHT, G, kFewFrags, GATED, OUT_FP8, true>(P, it, pool);
+      } else {
+        // the run's last strips, fewer than a wavefront holds
+        do_item_rows<WEIGHT, G, GATED ? 2 : 1, GATED, OUT_FP8, true>(P, it, pool);
+      }
+      unit += done;
     }
-    unit += done;
-    left -= done;
+    u = tile_end;
   }
 }
 
@@ -637,16 +642,18 @@ __global__ void __launch_bounds__(kFewWaves * 64, 2) gemm_few_kernel(const GemmP
   __shared__ uint32_t scan[kFewWaves];
   __shared__ __align__(16) uint8_t pool[kPoolBytes];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
-  tile_prefix<kFewWaves * 64, true>(P, most, pre, scan);
-  const uint32_t tiles = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
+  tile_prefix<kFewWaves * 64>(P, pre, scan, [=](int rows) {
+    return tiles_cost<WEIGHT>(few_rows(rows, most));
+  });
+  const uint32_t places = (uint32_t)__builtin_amdgcn_readfirstlane((int)pre[P.num_experts]);
   const int units = OUT_FP8 ? P.n / 128 : (P.n + 15) / 16;
-  const uint64_t total = (uint64_t)tiles * units;
+  const uint64_t total = (uint64_t)places * units;
   // Workgroups are dealt to the XCDs in turn; neighbours in the list, which
   // share rows of A, go to one XCD and its L2.
   constexpr int LOG = kFewBlocksLog2;
   const uint32_t at = (blockIdx.x % kXcds << LOG) / kXcds + blockIdx.x / kXcds;
   const uint64_t u0 = total * at >> LOG, u1 = total * (at + 1) >> LOG;
-  if (OUT_FP8 || total >> LOG >= kFewLong * (GATED ? kFewFrags / 2 : kFewFrags))
+  if (OUT_FP8 || total >> LOG >= 8 * kFewLong * (GATED ? kFewFrags / 2 : kFewFrags))
     do_run<WEIGHT, G, GATED, OUT_FP8, false>(P, most, pre, pool, units, u0, u1);
   else
     do_run<WEIGHT, G, GATED, OUT_FP8, true>(P, most, pre, pool, units, u0, u1);

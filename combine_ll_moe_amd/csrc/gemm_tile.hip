@@ -169,7 +169,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
   __shared__ __align__(16) uint8_t step0[2 * kHalf];
   __shared__ __align__(16) uint8_t step1[2 * kHalf];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
-  tile_prefix<kThreads, false>(P, most, pre, scan);
+  tile_prefix<kThreads>(P, pre, scan, [=](int rows) { return big_tiles(rows, most); });
   const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
@@ -331,7 +331,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_int4_kernel(const GemmP
   __shared__ __align__(16) uint8_t a0[kHalf], a1[kHalf], w0[kTile * 32], w1[kTile * 32];
   __shared__ __align__(16) uint8_t ring[kTile * (kRing + kZeroRing)];
   uint32_t* pre = reinterpret_cast<uint32_t*>(lds_raw);
-  tile_prefix<kThreads, false>(P, most, pre, scan);
+  tile_prefix<kThreads>(P, pre, scan, [=](int rows) { return big_tiles(rows, most); });
   const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1;
