@@ -102,6 +102,8 @@ __device__ __forceinline__ int strip_rows(const GemmParams& P, const Item& it, i
 // one row's scales and 8 of its zero points, whole aligned blocks, into a
 // ring of two blocks a row in LDS, and every lane reads its rows' values from
 // there. A row starts anywhere in a block: a window of 8 groups touches two.
+// Rows 16 apart start alike (and n, a multiple of 8, apart too), so a lane
+// reads every strip at the same place of its row.
 template <int NF, bool GATED>
 struct ScaleRing {
   static constexpr int kRow = 48, kZeroRow = 24;  // LDS bytes of a row, spread over the banks
@@ -111,8 +113,9 @@ struct ScaleRing {
   uint32_t block, zblock;       // this lane's next block's offset
   v4u next, head[2];
   v2u znext, zhead[2];
-  uint32_t at[NF], zat[NF];     // LDS: row f * 16 + lane % 16
-  uint32_t phase[NF], zphase[NF];
+  const uint8_t* mine;          // LDS: row lane % 16
+  const uint8_t* zmine;
+  uint32_t phase;               // of this row's first group in its block
   float none;
   int lane;
   static_assert(kBytes <= kRingBytes);
@@ -131,14 +134,9 @@ struct ScaleRing {
     const uint32_t g0 = (uint32_t)(strip_row<NF, GATED>(P, it.strip, hi % NF) + lo) * groups + first;
     block = 2 * g0 & ~15u;
     zblock = g0 & ~7u;
-#pragma unroll
-    for (int f = 0; f < NF; ++f) {
-      const uint32_t g = (uint32_t)(strip_row<NF, GATED>(P, it.strip, f) + lo) * groups + first;
-      at[f] = (f * 16 + lo) * kRow;
-      zat[f] = 64 * kRow + (f * 16 + lo) * kZeroRow;
-      phase[f] = 2 * g & 15;
-      zphase[f] = g & 7;
-    }
+    phase = (uint32_t)(lo * groups + first) & 7;
+    mine = ring + lo * kRow;
+    zmine = ring + 64 * kRow + lo * kZeroRow;
     // three blocks at once: the first two to LDS, when `settle` is called
     fetch();
     head[0] = next, zhead[0] = znext;
@@ -170,10 +168,10 @@ struct ScaleRing {
   }
   __device__ __forceinline__ float scale(int f, int g) const {
     return __uint_as_float(
-        (uint32_t) * reinterpret_cast<const uint16_t*>(lds + at[f] + ((phase[f] + 2 * g) & 31)) << 16);
+        (uint32_t) * reinterpret_cast<const uint16_t*>(mine + ((phase + g) & 15) * 2 + f * 16 * kRow) << 16);
   }
   __device__ __forceinline__ float zero(int f, int g) const {
-    return none + (float)lds[zat[f] + ((zphase[f] + g) & 15)];
+    return none + (float)zmine[((phase + g) & 15) + f * 16 * kZeroRow];
   }
 };
 

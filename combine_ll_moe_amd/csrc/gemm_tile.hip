@@ -395,14 +395,10 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_int4_kernel(const GemmP
       *reinterpret_cast<v4u*>(ring + tid * kRing + (b & 3) * 16) = next;
       *reinterpret_cast<v2u*>(ring + kTile * kRing + tid * kZeroRing + (b & 3) * 8) = znext;
     };
-    // this lane's row of each fragment: LDS place and phase
-    uint32_t r_at[8], r_phase[8];
-#pragma unroll
-    for (int f = 0; f < 8; ++f) {
-      const int i = frag_row<GATED>(wn, f) + lo;
-      r_at[f] = (uint32_t)i;
-      r_phase[f] = (uint32_t)weight_row(i) * groups & 7;
-    }
+    // rows 16 apart start alike in their blocks, and n, a multiple of 8, apart
+    const uint32_t phase = (uint32_t)(lo * groups) & 7;
+    const uint8_t* ring_at = ring + lo * kRing;
+    const uint8_t* zring_at = ring + kTile * kRing + lo * kZeroRing;
 
     f32x4 acc[4][8];
 #pragma unroll
@@ -438,11 +434,12 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_int4_kernel(const GemmP
               p[m] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(a[m][j], wf, j == u ? zero : p[m], 0, 0, 0);
           }
           const int g = G == 128 ? step >> 1 : step * GROUPS + u;
-          const uint32_t at = r_phase[f] + (uint32_t)g;
+          const uint32_t at = phase + (uint32_t)g;
+          const int row = frag_row<GATED>(wn, f);
           const float read = __uint_as_float(
-              (uint32_t) * reinterpret_cast<const uint16_t*>(ring + r_at[f] * kRing + (2 * at & 63)) << 16);
+              (uint32_t) * reinterpret_cast<const uint16_t*>(ring_at + 2 * (at & 31) + row * kRing) << 16);
           const float sc = G == 128 || g < groups ? read : 0.0f;
-          const float off = z_none + (float)ring[kTile * kRing + r_at[f] * kZeroRing + (at & 31)];
+          const float off = z_none + (float)zring_at[(at & 31) + row * kZeroRing];
 #pragma unroll
           for (int m = 0; m < 4; ++m)
 #pragma unroll
