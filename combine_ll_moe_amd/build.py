@@ -12,9 +12,9 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
 CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libllmoe.so")
-SOURCES = ["api.hip", "dispatch.hip", "combine.hip", "two_phase.hip", "receive.hip", "watch.hip",
-           "probe.hip", "expert_api.hip", "gemm_few.hip",
-           "gemm_tile.hip", "norm.hip"]
+SOURCES = ["gemm_few_int4.hip", "gemm_tile.hip", "gemm_few_fp8.hip", "gemm_few_bf16.hip",  # longest first
+           "api.hip", "dispatch.hip", "combine.hip", "two_phase.hip", "receive.hip", "watch.hip",
+           "probe.hip", "expert_api.hip", "norm.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

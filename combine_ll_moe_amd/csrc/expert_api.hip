@@ -46,14 +46,23 @@ bool gemm_sizes(int max_tokens, int n, int k, int num_experts, int act) {
   return act == LL_MOE_ACT_NONE || act == LL_MOE_ACT_SILU_MUL;
 }
 
-// XXX
-constexpr int kFewRowsMost = 64;
+// One launch or two. The few kernel takes experts of up to kFewRows rows, the
+// tile kernel those of more (64 experts of 4096 x 1536 bf16 weights, 100 rows
+// each: 209 us in tiles against 295 in the few kernel, which reads the weights
+// twice; the same for fp8, 300 against 476 with 7168 x 2048). Where no expert
+// can have as many, one launch does. An empty second launch takes 4 us: calls
+// that are short themselves, with at most 128 rows an expert and less than 256
+// MiB of weights, do without it and leave every row to the few kernel (8
+// experts of 1024 x 1024: 9.4 us against 13).
+constexpr uint64_t kTileWeights = 256ull << 20;
 
 int launch_gemm(const GemmParams& p, hipStream_t stream) {
-  if (p.max_tokens <= 128)
+  const uint64_t weights = (uint64_t)p.num_experts * (p.gated ? 2 : 1) * p.n * p.k;
+  const uint64_t bytes = p.weight == kWeightBf16 ? 2 * weights : p.weight == kWeightFp8 ? weights : weights / 2;
+  if (p.max_tokens <= kFewRows || (p.max_tokens <= 2 * kFewRows && bytes < kTileWeights))
     return from_hip(launch_gemm_few(p, INT32_MAX, stream));
-  const hipError_t e = launch_gemm_few(p, kFewRowsMost, stream);
-  return from_hip(e != hipSuccess ? e : launch_gemm_tile(p, kFewRowsMost, stream));
+  const hipError_t e = launch_gemm_few(p, kFewRows, stream);
+  return from_hip(e != hipSuccess ? e : launch_gemm_tile(p, kFewRows, stream));
 }
 
 }  // namespace

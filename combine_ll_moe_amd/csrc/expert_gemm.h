@@ -35,9 +35,10 @@ struct GemmParams {
 constexpr int kGemmMaxExperts = 4096;
 
 // LDS of the tile prefix below: a word an expert and the total, then the
-// experts' rows.
+// experts' rows (up to kRowsKept experts; the tiles' buffers leave no more).
+constexpr int kRowsKept = 2048;
 inline uint32_t tile_prefix_bytes(int num_experts) {
-  return ((uint32_t)(2 * num_experts + 1) * 4u + 15u) & ~15u;
+  return ((uint32_t)(num_experts + 1 + (num_experts <= kRowsKept ? num_experts : 0)) * 4u + 15u) & ~15u;
 }
 
 // Who takes which rows. An expert with at most `most` rows is the few kernel's,
@@ -92,7 +93,7 @@ __device__ __forceinline__ uint32_t wave_sums(uint32_t v) {
 }
 
 // What stands before each expert: pre[e], e <= E, of measure(rows), such as
-// its row tiles; the rows of each expert behind them. All THREADS threads
+// its row tiles; the rows of each expert behind them (kRowsKept). All THREADS threads
 // call it; scan: one word a wavefront.
 template <int THREADS, class Measure>
 __device__ __forceinline__ void tile_prefix(const GemmParams& P, uint32_t* pre, uint32_t* scan,
@@ -106,7 +107,7 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, uint32_t* pre, 
     c = c < P.max_tokens ? c : P.max_tokens;
     const uint32_t t = (uint32_t)measure(c);
     pre[e] = sum;
-    pre[E + 1 + e] = (uint32_t)c;
+    if (E <= kRowsKept) pre[E + 1 + e] = (uint32_t)c;
     sum += t;
   }
   const uint32_t incl = wave_sums(sum);
@@ -117,6 +118,18 @@ __device__ __forceinline__ void tile_prefix(const GemmParams& P, uint32_t* pre, 
   for (int e = e0; e < e1; ++e) pre[e] += base;
   if (tid == THREADS - 1) pre[E] = base + sum;
   __syncthreads();
+}
+
+// Rows of expert e (the same for the whole workgroup).
+__device__ __forceinline__ int rows_of(const GemmParams& P, const uint32_t* pre, int e) {
+  int c;
+  if (P.num_experts <= kRowsKept) {
+    c = (int)pre[P.num_experts + 1 + e];
+  } else {
+    c = P.counts[e];
+    c = c < P.max_tokens ? c : P.max_tokens;
+  }
+  return __builtin_amdgcn_readfirstlane(c);
 }
 
 // Expert of tile t < pre[E]: as many as have their last tile before t. All
@@ -208,6 +221,8 @@ __device__ __forceinline__ uint32_t e4m3_pack4(float p0, float p1, float p2, flo
 
 // Each takes its rows of every expert (few_rows, big_tiles).
 hipError_t launch_gemm_few(const GemmParams& p, int most, hipStream_t stream);
+hipError_t launch_gemm_few_fp8(const GemmParams& p, int most, hipStream_t stream);
+hipError_t launch_gemm_few_int4(const GemmParams& p, int most, hipStream_t stream);
 hipError_t launch_gemm_tile(const GemmParams& p, int most, hipStream_t stream);
 
 }  // namespace llmoe

@@ -23,6 +23,8 @@
 // any number of experts fill the GPU alike. Where the list is long, a
 // workgroup's wavefronts take strips beside each other over all of k; where
 // it is short, they split k and add their sums up in LDS.
+#pragma once
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -600,7 +602,7 @@ __device__ __forceinline__ void do_run(const GemmParams& P, int most, const uint
     // division in 32 bits wherever the list allows it
     const uint32_t at = u1 >> 32 ? (uint32_t)(u / (uint32_t)units) : (uint32_t)u / (uint32_t)units;
     const int e = expert_of_tile(pre, P.num_experts, at);
-    const int c = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + e]);
+    const int c = rows_of(P, pre, e);
     const uint64_t first = (uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)pre[e]) * units;
     const uint32_t in_e = (uint32_t)(u - first);
     const int t = (int)(in_e / full);
@@ -686,25 +688,4 @@ hipError_t launch(const GemmParams& p, int most, hipStream_t stream) {
 }
 
 }  // namespace
-
-hipError_t launch_gemm_few(const GemmParams& p, int most, hipStream_t stream) {
-  if (p.weight == kWeightFp8) {
-    if (p.out_fp8) return launch<kWeightFp8, 128, true, true>(p, most, stream);
-    return p.gated ? launch<kWeightFp8, 128, true, false>(p, most, stream)
-                   : launch<kWeightFp8, 128, false, false>(p, most, stream);
-  }
-  if (p.weight == kWeightInt4) {
-    if (p.group == 128)
-      return p.gated ? launch<kWeightInt4, 128, true, false>(p, most, stream)
-                     : launch<kWeightInt4, 128, false, false>(p, most, stream);
-    if (p.group == 64)
-      return p.gated ? launch<kWeightInt4, 64, true, false>(p, most, stream)
-                     : launch<kWeightInt4, 64, false, false>(p, most, stream);
-    return p.gated ? launch<kWeightInt4, 32, true, false>(p, most, stream)
-                   : launch<kWeightInt4, 32, false, false>(p, most, stream);
-  }
-  return p.gated ? launch<kWeightBf16, 128, true, false>(p, most, stream)
-                 : launch<kWeightBf16, 128, false, false>(p, most, stream);
-}
-
 }  // namespace llmoe

@@ -1,7 +1,7 @@
 // Products grouped by expert, for experts with many rows: tiles of 256 rows
 // and 256 weight rows on the matrix cores.
 //
-// Mathematics: as gemm_few.hip, P = A W^T over an expert's rows. fp8 with a
+// Mathematics: as gemm_few.h, P = A W^T over an expert's rows. fp8 with a
 // bf16 output: one 16x16x128 product per 128 columns, whose sum is scaled by
 // the activation's and the weight's scale and added up in fp32. The matrix
 // cores keep a sum of fp8 products to about 6e-6 of the products' magnitudes
@@ -154,7 +154,7 @@ __device__ __forceinline__ Tile tile_at(const GemmParams& P, const uint32_t* pre
   const int wide = across - 4 * group < 4 ? across - 4 * group : 4;
   const int in_g = (int)(in_e - 4ull * down * group);
   const int rt = in_g / wide, ct = 4 * group + in_g % wide;
-  const int left = __builtin_amdgcn_readfirstlane((int)pre[P.num_experts + 1 + o.e]) - rt * kTile;
+  const int left = rows_of(P, pre, o.e) - rt * kTile;
   o.rows = left < kTile ? left : kTile;
   o.row0 = (int64_t)o.e * P.max_tokens + (int64_t)rt * kTile;
   o.col0 = ct * COLS;
@@ -317,7 +317,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
 
 // The same tiles with 4-bit weights. A k step is 64 columns: 32 KiB of A and
 // 8 KiB of codes. The sums of a step (of half a step for groups of 32) are
-// scaled and added up as gemm_few.hip does; sum x comes from one product with
+// scaled and added up as gemm_few.h does; sum x comes from one product with
 // ones a fragment of rows. Scales and zero points of the tile's 256 weight rows
 // come in blocks of 8 groups into a ring of four blocks a row: a window of 8
 // groups reads two of them, starting anywhere in the first, while the block

@@ -2,9 +2,9 @@
 fails validation before anything is enqueued."""
 import pytest
 
-import combine_ll_moe_amd as ll
+torch = pytest.importorskip("torch")  # first: its HIP runtime is the one that the library then uses
 
-torch = pytest.importorskip("torch")
+import combine_ll_moe_amd as ll  # noqa: E402
 
 M = 1 << 32  # addresses far apart, never dereferenced
 

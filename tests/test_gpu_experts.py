@@ -172,6 +172,14 @@ def test_many_rows(c):
     Gemm(counts=[700, 5, 129, 256, 257, 0], cap=700, n=384, k=640, seed=3, **c).run().check()
 
 
+@pytest.mark.parametrize("kind", ["bf16", "fp8", "w4"])
+def test_capacity_of_128_with_large_weights(kind):
+    """Up to 128 rows an expert, weights of over 256 MiB."""
+    n, k = (4096, 4096) if kind == "bf16" else (8192, 4096) if kind == "fp8" else (8192, 8192)
+    _say(kind=kind, n=n, k=k)
+    Gemm(kind, [128, 3, 0, 65, 100, 64, 1, 17, 0, 90], 128, n, k, seed=9).run().check()
+
+
 @pytest.mark.parametrize("c", KINDS, ids=IDS)
 def test_no_rows_at_all(c):
     _say(**c)
@@ -184,6 +192,9 @@ def test_largest_expert_count(kind):
     counts[0], counts[4095], counts[2000] = 2, 2, 1
     _say(kind=kind, experts=4096)
     Gemm(kind, counts, 2, 16, 128).run().check(experts=[0, 2000, 4095])
+    # and with whole row tiles
+    counts[0], counts[4095] = 300, 150
+    Gemm(kind, counts, 300, 16, 128).run().check(experts=[0, 2000, 4095])
 
 
 @pytest.mark.parametrize("c", KINDS, ids=IDS)
