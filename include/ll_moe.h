@@ -354,9 +354,13 @@ int ll_moe_clean_signals(void* layout, int max_tokens, int hidden,
  * output, and its first counts[e] rows are filled (a count below 0 is taken
  * as 0, one above max_tokens as max_tokens). The counts are read on the
  * device when the call runs. Rows behind the count are neither read nor
- * written, and weights of an expert without rows are not read. A product of
- * a row depends on that row and the weights alone (a NaN or infinity stays
- * in its row).
+ * written, and weights of an expert without rows are not read. A row's
+ * products are of that row and the weights alone (a NaN or infinity stays
+ * in its row); how its sum over k is grouped, and so its last bits, goes by
+ * the counts of the call. The same call gives the same bits.
+ * The products enqueue one or two kernels. No call needs a workspace, so
+ * calls may run at once on several streams. All may be captured; a replay
+ * reads the counts as they are then.
  */
 #define LL_MOE_FP32 2                /* ll_moe_rms_norm: x in fp32 */
 #define LL_MOE_ACT_NONE 0
@@ -365,7 +369,9 @@ int ll_moe_clean_signals(void* layout, int max_tokens, int hidden,
 
 /*
  * ll_moe_expert_gemm - products grouped by expert, bf16 or fp8.
- * For every filled row r of expert e, with fp32 sums,
+ * For every filled row r of expert e, with fp32 sums (fp8 with a bf16 output
+ * and more than 64 rows: the matrix cores' sums of 128 fp8 products, good to
+ * about 6e-6 of the products' magnitudes, are scaled and summed in fp32),
  *   P[r, i] = sum over c < k of A[r, c] * W[e, i, c]
  *   ACT_NONE:     out[r, i] = P[r, i], i < n (W_e has n rows)
  *   ACT_SILU_MUL: out[r, i] = g / (1 + exp(-g)) * u with g = P[r, i],
