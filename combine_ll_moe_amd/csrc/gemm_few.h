@@ -7,8 +7,7 @@
 //   fp8:  codes become bf16, which holds them exactly, on their way to the
 //         same products; the sum of 128 columns is scaled by the activation's
 //         and the weight's scale and added up in fp32. (The matrix cores' own
-//         fp8 products keep a sum to about 6e-6 of its magnitudes, and here
-//         there is time to spare.)
+//         fp8 products keep a sum to about 6e-6 of its magnitudes only.)
 //   int4: W = s (c - z), c the code, z the zero point, s the group's scale.
 //         With c' = 16 + c, which bf16 holds exactly as 0x4180 | c << 3,
 //         sum x W = s (sum x c' - (16 + z) sum x): codes become bf16 with a

@@ -1,14 +1,13 @@
 // Products grouped by expert, for experts with many rows: tiles of 256 rows
 // and 256 weight rows on the matrix cores.
 //
-// Mathematics: as gemm_few.h, P = A W^T over an expert's rows. fp8 with a
-// bf16 output: one 16x16x128 product per 128 columns, whose sum is scaled by
-// the activation's and the weight's scale and added up in fp32. The matrix
-// cores keep a sum of fp8 products to about 6e-6 of the products' magnitudes
-// (measured over 128 columns; a bf16 product to fp32's rounding); a bf16
-// output's own rounding is 2^-9 of it on average. The fp8 output comes with
-// fp32 scales, which would show it: there the codes become bf16, which holds
-// them exactly, and go through bf16 products at half the rate.
+// Mathematics: as gemm_few.h, P = A W^T over an expert's rows. fp8 codes
+// become bf16, which holds them exactly, and go through bf16 products at half
+// the rate: the matrix cores keep a sum of fp8 products to about 6e-6 of the
+// products' magnitudes only (measured over 128 columns, of one 128-column
+// product and of four 32-column ones), a bf16 product to fp32's rounding. With
+// fp8 products a bf16 output was rounded to another value than the exact
+// sum's 80 times as often, and went by which kernel a row fell to.
 //
 // Design: eight wavefronts, 4 x 2, each 64 rows by 128 weight rows. A k step
 // is 128 bytes of every row (64 bf16, 128 fp8): 64 KiB, copied from memory
@@ -22,9 +21,10 @@
 //
 // Bound: the copies, which land later than a step's products end. 8 experts of
 // 2048 rows, 4096 x 4096, gated: bf16 546-612 us (900-1007 TFLOP/s), of which
-// 430 remain without any copy; fp8 with a bf16 output 400-419 us (1310-1374
-// TFLOP/s); 4-bit weights 825-859 us (640-667 TFLOP/s), where the scaling of
-// every group's sums adds vector instructions.
+// 430 remain without any copy; 4-bit weights 825-859 us (640-667 TFLOP/s),
+// where the scaling of every group's sums adds vector instructions. fp8, where
+// the codes' conversion does: 547 us without the gate (1000 TFLOP/s; 412 with
+// fp8 products), with it 1342 us to bf16 (820; 856) and 1268 to fp8 (867).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -86,7 +86,7 @@ __device__ __forceinline__ int frag_row(int wn, int f) {
 
 // One k step. acc[m][f]: lane l holds weight rows 4 (l / 16) + r of fragment
 // f for row l % 16 of row fragment m.
-template <int WEIGHT, bool GATED, bool OUT_FP8>
+template <int WEIGHT, bool GATED>
 __device__ __forceinline__ void multiply(const uint8_t* lds, int wm, int wn, const float (&as)[4],
                                          const float (&ws)[3], int edge, f32x4 (&acc)[4][8]) {
   const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
@@ -108,36 +108,37 @@ __device__ __forceinline__ void multiply(const uint8_t* lds, int wm, int wn, con
               __builtin_bit_cast(bf16x8, w[f]), __builtin_bit_cast(bf16x8, a[m]), acc[m][f], 0, 0, 0);
     }
   } else {
-    v4u a[4][2];
+    // Gated: the step's halves in turn, for the registers (8 experts of 2048
+    // rows, 4096 x 4096, out in bf16: 1365 us against 1454, fp8 1296 against
+    // 1294; plain, where the halves' own scaling costs more, 610 against 561).
+    constexpr int HALVES = GATED ? 2 : 1, CHUNKS = 2 / HALVES;
 #pragma unroll
-    for (int m = 0; m < 4; ++m)
+    for (int h = 0; h < HALVES; ++h) {
+      Bf16x16 a[4][CHUNKS];
 #pragma unroll
-      for (int j = 0; j < 2; ++j) a[m][j] = chunk_of(la, wm * 64 + m * 16 + lo, 4 * j + hi);
+      for (int m = 0; m < 4; ++m)
 #pragma unroll
-    for (int f = 0; f < 8; ++f) {
-      v4u w[2];
+        for (int j = 0; j < CHUNKS; ++j)
+          a[m][j] = fp8_to_bf16(chunk_of(la, wm * 64 + m * 16 + lo, 4 * (h + j) + hi));
 #pragma unroll
-      for (int j = 0; j < 2; ++j) w[j] = chunk_of(lw, frag_row<GATED>(wn, f) + lo, 4 * j + hi);
+      for (int f = 0; f < 8; ++f) {
+        Bf16x16 w[CHUNKS];
 #pragma unroll
-      for (int m = 0; m < 4; ++m) {
-        f32x4 p = {0, 0, 0, 0};
-        if constexpr (OUT_FP8) {
+        for (int j = 0; j < CHUNKS; ++j)
+          w[j] = fp8_to_bf16(chunk_of(lw, frag_row<GATED>(wn, f) + lo, 4 * (h + j) + hi));
 #pragma unroll
-          for (int j = 0; j < 2; ++j) {
-            const Bf16x16 wb = fp8_to_bf16(w[j]), ab = fp8_to_bf16(a[m][j]);
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.lo, ab.lo, p, 0, 0, 0);
-            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wb.hi, ab.hi, p, 0, 0, 0);
+        for (int m = 0; m < 4; ++m) {
+          f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+          for (int j = 0; j < CHUNKS; ++j) {
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j].lo, a[m][j].lo, p, 0, 0, 0);
+            p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j].hi, a[m][j].hi, p, 0, 0, 0);
           }
-        } else {
-          auto join = [](const v4u (&v)[2]) {
-            return i32x8{(int)v[0].x, (int)v[0].y, (int)v[0].z, (int)v[0].w,
-                         (int)v[1].x, (int)v[1].y, (int)v[1].z, (int)v[1].w};
-          };
-          p = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(join(w), join(a[m]), p, 0, 0, 0, 0, 0, 0);
-        }
-        const float sc = as[m] * ws[!GATED || f < 4 ? 0 : f - 4 < edge ? 1 : 2];
+          const float sc = as[m] * ws[!GATED || f < 4 ? 0 : f - 4 < edge ? 1 : 2];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[m][f][r] = __builtin_fmaf(sc, p[r], acc[m][f][r]);
+          for (int r = 0; r < 4; ++r) acc[m][f][r] = __builtin_fmaf(sc, p[r], acc[m][f][r]);
+        }
+        if (!GATED) __builtin_amdgcn_sched_barrier(0);  // fragments in turn, for the registers
       }
     }
   }
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
         copy_step(s, k + 1, step1, wave);
         scales(k + 1, as[1], ws[1]);
       }
-      if (busy) multiply<WEIGHT, GATED, OUT_FP8>(step0, wm, wn, as[0], ws[0], edge, acc);
+      if (busy) multiply<WEIGHT, GATED>(step0, wm, wn, as[0], ws[0], edge, acc);
       __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
       __syncthreads();
       if (k + 1 >= steps) break;
@@ -260,7 +261,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
         copy_step(s, k + 2, step0, wave);
         scales(k + 2, as[0], ws[0]);
       }
-      if (busy) multiply<WEIGHT, GATED, OUT_FP8>(step1, wm, wn, as[1], ws[1], edge, acc);
+      if (busy) multiply<WEIGHT, GATED>(step1, wm, wn, as[1], ws[1], edge, acc);
       __builtin_amdgcn_s_waitcnt(kWaitVmcnt0);
       __syncthreads();
     }
