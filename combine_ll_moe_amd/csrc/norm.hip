@@ -129,13 +129,35 @@ __global__ void __launch_bounds__(ROW < 256 ? 256 : ROW) norm_kernel(const NormP
   }
 }
 
+// The norm of `rows` rows from row `first` on.
+NormParams rows_from(const NormParams& p, uint64_t first, int rows) {
+  NormParams q = p;
+  const uint64_t at = first * p.hidden;
+  q.x += at * (p.x_fp32 ? 4 : 2);
+  if (q.residual) q.residual += at * 2;
+  if (q.residual_out) q.residual_out += at * 2;
+  q.out += at * (p.out_fp8 ? 1 : 2);
+  if (p.out_fp8) q.out_scales += at / 128;
+  q.num_tokens = rows;
+  return q;
+}
+
 template <int ROW, int C, bool X_FP32, bool RESIDUAL>
 hipError_t launch(const NormParams& p, hipStream_t stream) {
   constexpr int BLOCK = ROW < 256 ? 256 : ROW, ROWS = BLOCK / ROW;
-  const unsigned blocks = (unsigned)(((int64_t)p.num_tokens + ROWS - 1) / ROWS);
-  if (p.out_fp8) norm_kernel<ROW, C, X_FP32, RESIDUAL, true><<<blocks, BLOCK, 0, stream>>>(p);
-  else norm_kernel<ROW, C, X_FP32, RESIDUAL, false><<<blocks, BLOCK, 0, stream>>>(p);
-  return hipGetLastError();
+  // A grid has fewer than 2^32 threads (one of more is cut off without an
+  // error): 2^31 threads a launch, 2^21 rows of 1024 threads at the least.
+  constexpr int kMost = (int)((1ll << 31) / ROW);
+  for (int64_t first = 0; first < p.num_tokens; first += kMost) {
+    const int64_t left = p.num_tokens - first;
+    const NormParams q = rows_from(p, (uint64_t)first, (int)(left < kMost ? left : kMost));
+    const unsigned blocks = ((unsigned)q.num_tokens + ROWS - 1) / ROWS;
+    if (q.out_fp8) norm_kernel<ROW, C, X_FP32, RESIDUAL, true><<<blocks, BLOCK, 0, stream>>>(q);
+    else norm_kernel<ROW, C, X_FP32, RESIDUAL, false><<<blocks, BLOCK, 0, stream>>>(q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
 }
 
 template <bool X_FP32, bool RESIDUAL>

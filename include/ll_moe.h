@@ -435,7 +435,8 @@ int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_experts, int gro
  *                 aligned; residual and residual_out bf16, either may be NULL.
  *   weight:       device bf16 [hidden], 16-byte aligned.
  *   out_scales:   device fp32 [num_tokens, hidden / 128] (fp8 only).
- *   num_tokens >= 0 (0 enqueues nothing), hidden % 8 == 0, hidden <= 32768,
+ *   num_tokens >= 0 (0 enqueues nothing, more than 2^21 may be several
+ *   kernels, one after the other), hidden % 8 == 0, hidden <= 32768,
  *   eps finite and >= 0. residual_out may be residual itself; apart from that
  *   outputs may overlap neither an input nor each other. Enqueued on `stream`.
  */
