@@ -48,7 +48,7 @@ def build(verbose: bool = False, extra_flags=None) -> str:
         with ThreadPoolExecutor(min(6, os.cpu_count() or 1)) as pool:
             list(pool.map(run, ([hipcc, *[f for f in flags if f != "-shared"], "-c", "-o", o,
                                  os.path.join(CSRC, s)] for s, o in zip(SOURCES, objects))))
-        run([hipcc, *FLAGS, "-o", LIB + ".tmp", *objects])
+        run([hipcc, *FLAGS, *(extra_flags or []), "-o", LIB + ".tmp", *objects])
     os.replace(LIB + ".tmp", LIB)
     return LIB
 
