@@ -107,29 +107,40 @@ def _ptr(a):
     return a.data_ptr()
 
 
-def _operands(call: str, stream, *tensors) -> list:
+_ANY = (0,) * 8
+_torch_c = None  # torch's C module, once a call has needed it
+
+
+def _operands(call: str, stream, *tensors, items=_ANY, sizes=_ANY) -> list:
     """Addresses of contiguous tensors on the current device (or raw addresses
     as they are), then the stream: the kernels take whole arrays and run where
-    the stream is. Torch's accessors of the device and the current stream make
+    the stream is. items, sizes: for each tensor the bytes of an element (0:
+    any) and the bytes that the call reads or writes; a tensor of another
+    element size or of fewer bytes is refused, as the kernels would go past
+    its end. Torch's accessors of the device and the current stream make
     Python objects, which takes longer than a small kernel; these return
     numbers."""
+    global _torch_c
     out, device = [], None
-    for a in tensors:
+    for a, item, size in zip(tensors, items, sizes):
         if a is None or type(a) is int:
             out.append(a)
             continue
         d = a.get_device()
-        if d < 0 or (device is not None and d != device) or not a.is_contiguous():
+        if (d < 0 or (device is not None and d != device) or not a.is_contiguous()
+                or a.nbytes < size or (item and a.element_size() != item)):
             raise LLMoEError(INVALID_ARGUMENT, call)
         device = d
         out.append(a.data_ptr())
     if device is None:
         out.append(_stream(stream))
         return out
-    from torch import _C
-    if device != _C._cuda_getDevice():
+    if _torch_c is None:
+        from torch import _C
+        _torch_c = _C
+    if device != _torch_c._cuda_getDevice():
         raise LLMoEError(INVALID_ARGUMENT, call)
-    out.append(_C._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
+    out.append(_torch_c._cuda_getCurrentRawStream(device) if stream is None else _stream(stream))
     return out
 
 
@@ -202,30 +213,53 @@ def ll_moe_expert_gemm(max_tokens: int, n: int, k: int, num_experts: int, dtype:
                        out_dtype: int, a, a_scales, w, w_scales, counts, out, out_scales=None,
                        stream=None) -> None:
     """Products grouped by expert (bf16 or fp8), plain or gated. Tensors are
-    contiguous and on the current device."""
+    contiguous, on the current device, of the operand's element size and at
+    least as large."""
+    rows, rows_w = num_experts * max_tokens, 2 * n if act else n
+    fp8, fp8_out = dtype == FP8_E4M3, out_dtype == FP8_E4M3
+    item, out_item = 1 if fp8 else 2, 1 if fp8_out else 2
+    scale, out_scale = 4 if fp8 else 0, 4 if fp8_out else 0  # operands that are ignored: any
+    kb = k // 128
+    items = (item, scale, item, scale, 4, out_item, out_scale)
+    sizes = (item * rows * k, scale * rows * kb, item * num_experts * rows_w * k,
+             scale * num_experts * ((rows_w + 127) // 128) * kb, 4 * num_experts,
+             out_item * rows * n, out_scale * rows * (n // 128))
     _check(_lib.ll_moe_expert_gemm(max_tokens, n, k, num_experts, dtype, act, out_dtype,
                                    *_operands("ll_moe_expert_gemm", stream, a, a_scales, w,
-                                              w_scales, counts, out, out_scales)),
+                                              w_scales, counts, out, out_scales, items=items,
+                                              sizes=sizes)),
            "ll_moe_expert_gemm")
 
 
 def ll_moe_expert_gemm_w4(max_tokens: int, n: int, k: int, num_experts: int, group: int, act: int,
                           a, w, w_scales, w_zeros, counts, out, stream=None) -> None:
     """Products grouped by expert with 4-bit weights and a scale (and zero
-    point) a group. Tensors are contiguous and on the current device."""
+    point) a group. Tensors are contiguous, on the current device, of the
+    operand's element size and at least as large."""
+    rows, rows_w = num_experts * max_tokens, num_experts * (2 * n if act else n)
+    groups = rows_w * (k // group) if group > 0 else 0
+    sizes = (2 * rows * k, rows_w * (k // 2), 2 * groups, groups, 4 * num_experts, 2 * rows * n)
     _check(_lib.ll_moe_expert_gemm_w4(max_tokens, n, k, num_experts, group, act,
                                       *_operands("ll_moe_expert_gemm_w4", stream, a, w, w_scales,
-                                                 w_zeros, counts, out)),
+                                                 w_zeros, counts, out, items=(2, 1, 2, 1, 4, 2),
+                                                 sizes=sizes)),
            "ll_moe_expert_gemm_w4")
 
 
 def ll_moe_rms_norm(num_tokens: int, hidden: int, x_dtype: int, out_dtype: int, eps: float, x,
                     residual, weight, residual_out, out, out_scales=None, stream=None) -> None:
-    """Root-mean-square norm of x plus the residual. Tensors are contiguous
-    and on the current device."""
+    """Root-mean-square norm of x plus the residual. Tensors are contiguous, on
+    the current device, of the operand's element size and at least as large."""
+    values, x_item = num_tokens * hidden, 4 if x_dtype == FP32 else 2
+    if out_dtype == FP8_E4M3:
+        items = (x_item, 2, 2, 2, 1, 4)
+        sizes = (x_item * values, 2 * values, 2 * hidden, 2 * values, values, values // 32)
+    else:
+        items = (x_item, 2, 2, 2, 2, 0)
+        sizes = (x_item * values, 2 * values, 2 * hidden, 2 * values, 2 * values, 0)
     _check(_lib.ll_moe_rms_norm(num_tokens, hidden, x_dtype, out_dtype, eps,
                                 *_operands("ll_moe_rms_norm", stream, x, residual, weight,
-                                           residual_out, out, out_scales)),
+                                           residual_out, out, out_scales, items=items, sizes=sizes)),
            "ll_moe_rms_norm")
 
 
