@@ -9,6 +9,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include "kernels.h"
+
 namespace llmoe {
 
 enum : int { kWeightBf16 = 0, kWeightFp8 = 1, kWeightInt4 = 2 };
@@ -31,8 +33,6 @@ struct GemmParams {
   int gated;                // silu(gate) * up
   int out_fp8;
 };
-
-constexpr int kGemmMaxExperts = 4096;
 
 // LDS of the tile prefix below: a word an expert and the total, then the
 // experts' rows (up to kRowsKept experts; the tiles' buffers leave no more).
@@ -146,6 +146,12 @@ __device__ __forceinline__ int expert_of_tile(const uint32_t* pre, int E, uint32
   return base + __popcll(__ballot(e < E && pre[e < E ? e + 1 : E] <= t));
 }
 
+typedef __amdgpu_buffer_rsrc_t Rsrc;
+constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset behind every descriptor's range
+__device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
+}
+
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
@@ -206,7 +212,8 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
 }
 
 // fp32 -> OCP e4m3 codes, four packed little-endian: nearest even, +-448 for
-// everything beyond and for the infinities, 0x7F for NaN.
+// everything beyond and for the infinities, 0x7F for NaN. (As the dispatch's
+// encoder, without its branch around the NaN's patch.)
 __device__ __forceinline__ uint32_t e4m3_pack4(float p0, float p1, float p2, float p3) {
   const float c0 = __builtin_amdgcn_fmed3f(p0, -448.0f, 448.0f);
   const float c1 = __builtin_amdgcn_fmed3f(p1, -448.0f, 448.0f);

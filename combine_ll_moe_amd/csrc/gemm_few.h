@@ -15,13 +15,14 @@
 //         is one more matrix product, with ones, shared by all strips.
 //
 // Design: rows of W and A go through registers, several steps of k ahead, and
-// through LDS into the products (sum_item). Rows of A behind the expert's count, rows of W behind n and columns
-// behind k are beyond their buffer descriptors' range: those loads return
-// zeros and touch no memory. The strips of all experts form one list that is
-// dealt to the workgroups in equal runs, so experts of any count and calls of
-// any number of experts fill the GPU alike. Where the list is long, a
-// workgroup's wavefronts take strips beside each other over all of k; where
-// it is short, they split k and add their sums up in LDS.
+// through LDS into the products (sum_item). Rows of A behind the expert's
+// count, rows of W behind n and columns behind k are beyond their buffer
+// descriptors' range: those loads return zeros and touch no memory. The strips
+// of all experts form one list that is dealt to the workgroups in equal runs,
+// so experts of any count and calls of any number of experts fill the GPU
+// alike. Where the list is long, or the output fp8, a workgroup's wavefronts
+// take strips beside each other over all of k; else they split k and add their
+// sums up in LDS.
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -33,8 +34,6 @@
 namespace llmoe {
 namespace {
 
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-constexpr uint32_t kOutside = 0x7FFFFFF0u;  // an offset behind every descriptor's range
 constexpr int kFewFrags = 4;      // weight strips a wavefront holds at once
 constexpr int kFewWaves = 4;      // of a workgroup
 // From this many strips a wavefront (in units of what it holds at once) on,
@@ -48,9 +47,6 @@ static_assert(kPoolWave >= 64 * 128);
 constexpr int kPoolA = 32768;
 constexpr int kPoolBytes = kFewWaves * kPoolWave + kPoolA;
 
-__device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
-}
 template <int POLICY = 0>
 __device__ __forceinline__ v4u load16(Rsrc r, uint32_t off) {
   return __builtin_amdgcn_raw_buffer_load_b128(r, (int)off, 0, POLICY);

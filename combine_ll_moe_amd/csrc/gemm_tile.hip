@@ -34,16 +34,11 @@
 namespace llmoe {
 namespace {
 
-typedef __amdgpu_buffer_rsrc_t Rsrc;
-constexpr uint32_t kOutside = 0x7FFFFFF0u;
 constexpr int kTile = kTileRows;      // rows of a tile, and weight rows
 constexpr int kStepBytes = 128;       // of a row in a k step
 constexpr int kHalf = kTile * kStepBytes;
 constexpr int kThreads = 512;
 
-__device__ __forceinline__ Rsrc rsrc_of(const void* base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), 0, (int)bytes, kBufferWord3);
-}
 
 typedef __attribute__((address_space(3))) uint8_t LdsByte;
 
@@ -268,7 +263,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
 
     // outputs: a lane's four consecutive columns of one row
     constexpr int F = GATED ? 4 : 8;
-    float* most = reinterpret_cast<float*>(step0);  // fp8: amax of a row's half, [256][2]
+    float* amaxes = reinterpret_cast<float*>(step0);  // fp8: amax of a row's half, [256][2]
     if constexpr (GATED) {
 #pragma unroll
       for (int m = 0; m < 4; ++m)
@@ -287,7 +282,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
           for (int q = 0; q < 4; ++q) v = fmaxf(v, fabsf(acc[m][f][q]));  // NaN is ignored
         v = fmaxf(v, __shfl_xor(v, 16, 64));
         v = fmaxf(v, __shfl_xor(v, 32, 64));
-        if (hi == 0) most[(wm * 64 + m * 16 + lo) * 2 + wn] = v;
+        if (hi == 0) amaxes[(wm * 64 + m * 16 + lo) * 2 + wn] = v;
       }
       __syncthreads();
     }
@@ -298,7 +293,7 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
         const uint64_t orow = (uint64_t)(row0 + row);
         float inv = 0.0f;
         if constexpr (OUT_FP8) {
-          const float amax = fmaxf(most[row * 2], most[row * 2 + 1]);
+          const float amax = fmaxf(amaxes[row * 2], amaxes[row * 2 + 1]);
           inv = amax > 0.0f ? 448.0f / amax : 0.0f;
           if (wn == 0 && hi == 0)
             P.out_scales[orow * (P.n / 128) + col0 / 128] = amax > 0.0f ? amax / 448.0f : 0.0f;

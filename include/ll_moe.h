@@ -412,10 +412,13 @@ int ll_moe_expert_gemm(int max_tokens, int n, int k, int num_experts, int dtype,
  *   w_zeros:  device uint8 [num_experts, n or 2n, k / group], 8-byte aligned,
  *             or NULL: 8.
  *   out:      bf16.
- * An expert has fewer than 2^30 scales. No weight is rounded: a group's codes are multiplied and summed in fp32 and
- * the scale is applied to the sum. The sum is taken as sum((16 + code) * A) -
- * (16 + z) * sum(A): a row that holds an infinity (or magnitudes whose 31-fold
- * sums leave fp32's range) gives NaN. Everything else as ll_moe_expert_gemm.
+ * An expert has fewer than 2^30 scales. No weight is rounded: a group's codes
+ * are multiplied and summed in fp32 and the scale is applied to the sum. The
+ * sum is taken as sum((16 + code) * A) - (16 + z) * sum(A), so its error is
+ * fp32's of sums of (16 + code) * |A| and (16 + z) * |A|: a group whose weights
+ * are all zero (code = z) leaves a rounding of that size and not exactly zero.
+ * A row that holds an infinity (or magnitudes whose 31-fold sums leave fp32's
+ * range) gives NaN. Everything else as ll_moe_expert_gemm.
  */
 int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_experts, int group, int act,
                           const void* a, const void* w, const void* w_scales,
