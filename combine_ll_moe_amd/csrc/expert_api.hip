@@ -49,7 +49,7 @@ bool gemm_sizes(int max_tokens, int n, int k, int num_experts, int act) {
 // One launch or two. The few kernel takes experts of up to kFewRows rows, the
 // tile kernel those of more (64 experts of 4096 x 1536 bf16 weights, 100 rows
 // each: 209 us in tiles against 297 in the few kernel, which reads the weights
-// twice; the same for fp8, 300 against 476 with 7168 x 2048; 4-bit weights would be
+// twice; the same for fp8, 390 against 476 with 7168 x 2048; 4-bit weights would be
 // faster there, 217 against 276, and slower at uneven counts). Where no expert
 // can have as many, one launch does. An empty second launch takes 4 us: calls
 // that are short themselves, with at most 128 rows an expert and less than 256

@@ -20,11 +20,13 @@
 // SIMD holds wavefronts of two quarters.
 //
 // Bound: the copies, which land later than a step's products end. 8 experts of
-// 2048 rows, 4096 x 4096, gated: bf16 546-612 us (900-1007 TFLOP/s), of which
-// 430 remain without any copy; 4-bit weights 825-859 us (640-667 TFLOP/s),
-// where the scaling of every group's sums adds vector instructions. fp8, where
-// the codes' conversion does: 547 us without the gate (1000 TFLOP/s; 412 with
-// fp8 products), with it 1342 us to bf16 (820; 856) and 1268 to fp8 (867).
+// 2048 rows, 4096 weight rows x 4096 columns (calls one by one): bf16 548-554
+// us (992-1004 TFLOP/s; 430 remained without any copy of one run's 612), gated
+// 565-596; fp8, where the codes' conversion comes beside the products, 547-549
+// (fp8 products took 412), gated 591-612 to bf16 and 588-591 to fp8; 4-bit
+// weights, where the scaling of every group's sums adds vector instructions,
+// 839-853 in groups of 128 (645-655 TFLOP/s), gated 894-939, and 1140-1154 in
+// groups of 32.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -104,8 +106,9 @@ __device__ __forceinline__ void multiply(const uint8_t* lds, int wm, int wn, con
     }
   } else {
     // Gated: the step's halves in turn, for the registers (8 experts of 2048
-    // rows, 4096 x 4096, out in bf16: 1365 us against 1454, fp8 1296 against
-    // 1294; plain, where the halves' own scaling costs more, 610 against 561).
+    // rows, 8192 weight rows x 4096, to bf16 1365 us against 1454, to fp8 1296
+    // against 1294; plain, 4096 weight rows, where the halves' own scaling
+    // costs more, 610 against 561).
     constexpr int HALVES = GATED ? 2 : 1, CHUNKS = 2 / HALVES;
 #pragma unroll
     for (int h = 0; h < HALVES; ++h) {
