@@ -1,5 +1,6 @@
-"""Sums of the fp8 products on the GPU: fp32 in every kernel, so that a row's
-result does not depend on how many rows its expert has."""
+"""Sums of the fp8 and 4-bit products on the GPU: fp32 in every kernel, so that a
+row's result does not depend on how many rows its expert has; every code and
+zero point."""
 import pytest
 
 pytestmark = pytest.mark.gpu
@@ -10,6 +11,7 @@ if not torch.cuda.is_available():  # pragma: no cover - collected on CPU machines t
 
 import combine_ll_moe_amd as ll  # noqa: E402
 from _gpu import DEV, say  # noqa: E402
+from test_gpu_experts import Gemm  # noqa: E402
 
 BF16, F8 = torch.bfloat16, torch.float8_e4m3fn
 
@@ -56,3 +58,45 @@ def test_fp8_sums_are_fp32_in_every_kernel(gated, n, k):
         assert torch.equal(got[:300], want) and torch.equal(got[300:], want), \
             (int((got[:300] != want).sum()), int((got[300:] != want).sum()))
     assert torch.equal(got[:300], got[300:]), int((got[:300] != got[300:]).sum())
+
+
+@pytest.mark.parametrize("side", ["weights", "activations"])
+def test_every_e4m3_code(side):
+    """One product a sum: all 256 codes, subnormals and NaN among them, come out
+    as the values they stand for (bf16 holds each), in few rows and in tiles."""
+    say("case", side)
+    cap, n, k = 300, 256, 128
+    codes = torch.arange(256, dtype=torch.uint8, device=DEV)
+    one = torch.ones((), device=DEV).to(F8).view(torch.uint8)
+    counts = [300, 60]
+    x = torch.zeros(2 * cap, k, dtype=torch.uint8, device=DEV)
+    w = torch.zeros(2, n, k, dtype=torch.uint8, device=DEV)
+    if side == "weights":
+        x[:, 5], w[:, :, 5] = one, codes
+        want = codes.view(F8).float().expand(2 * cap, n)
+    else:
+        x[:, 5] = codes.repeat(3)[:2 * cap]
+        w[:, :, 5] = one
+        want = x[:, 5].view(F8).float()[:, None].expand(2 * cap, n)
+    out = torch.zeros(2 * cap, n, dtype=BF16, device=DEV)
+    ll.ll_moe_expert_gemm(cap, n, k, 2, ll.FP8_E4M3, ll.ACT_NONE, ll.BF16, x.view(F8), torch.ones(2 * cap, 1, device=DEV),
+                          w.view(F8), torch.ones(2, 2, 1, device=DEV),
+                          torch.tensor(counts, dtype=torch.int32, device=DEV), out)
+    torch.cuda.synchronize()
+    for rows in (slice(0, 300), slice(cap, cap + 60)):
+        got, ref = out[rows].float(), want[rows]
+        nan = torch.isnan(ref)
+        assert torch.equal(torch.isnan(got), nan) and torch.equal(got[~nan], ref[~nan])
+    assert not out[cap + 60:].any()
+
+
+@pytest.mark.parametrize("group", [32, 64, 128])
+@pytest.mark.parametrize("gated", [False, True])
+def test_zero_points_of_all_eight_bits(group, gated):
+    """Zero points are bytes: codes lie up to 255 below them. Few rows and
+    tiles, against 64 bits."""
+    say("case", group, gated)
+    g = Gemm("w4", [300, 60, 1], 300, 136, 3 * 128, gated=gated, group=group, zeros=True, seed=group)
+    gen = torch.Generator(device=DEV).manual_seed(1)
+    g.w_zeros = torch.randint(0, 256, g.w_zeros.shape, generator=gen, device=DEV, dtype=torch.uint8)
+    g.run().check()
