@@ -211,6 +211,18 @@ __device__ __forceinline__ float silu_mul(float g, float u) {
   return g / (1.0f + __expf(-g)) * u;
 }
 
+// Scale of 128 columns with largest magnitude amax, and what they are
+// multiplied by for their codes: amax / 448 and 448 / amax, as the dispatch
+// quantizes, but no scale below 2^-127: there 448 / amax would be infinite,
+// and a zero's code NaN (a row whose gates all lie below -86 has such values).
+struct BlockScale {
+  float scale, inv;
+};
+__device__ __forceinline__ BlockScale block_scale(float amax) {
+  if (!(amax > 0.0f)) return {0.0f, 0.0f};
+  return {fmaxf(amax / 448.0f, 0x1p-127f), fminf(448.0f / amax, 0x1p127f)};
+}
+
 // fp32 -> OCP e4m3 codes, four packed little-endian: nearest even, +-448 for
 // everything beyond and for the infinities, 0x7F for NaN. (As the dispatch's
 // encoder, without its branch around the NaN's patch.)

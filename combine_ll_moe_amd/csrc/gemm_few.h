@@ -554,11 +554,11 @@ __device__ __forceinline__ void do_item(const GemmParams& P, const Item& it, uin
         for (int r = 0; r < 4; ++r) amax = fmaxf(amax, fabsf(v[r]));  // NaN is ignored
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-        const float inv = amax > 0.0f ? 448.0f / amax : 0.0f;
+        const auto [scale, inv] = block_scale(amax);
         if (in) {
           *reinterpret_cast<uint32_t*>(P.out + orow * P.n + col) =
               e4m3_pack4(v[0] * inv, v[1] * inv, v[2] * inv, v[3] * inv);
-          if (c4 == 0) P.out_scales[orow * (P.n / 128) + col / 128] = amax > 0.0f ? amax / 448.0f : 0.0f;
+          if (c4 == 0) P.out_scales[orow * (P.n / 128) + col / 128] = scale;
         }
       } else if (in) {
         *reinterpret_cast<uint2*>(P.out + 2 * (orow * P.n + col)) =

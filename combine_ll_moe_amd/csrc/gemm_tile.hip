@@ -296,10 +296,9 @@ __global__ void __launch_bounds__(kThreads, 2) gemm_tile_kernel(const GemmParams
         const uint64_t orow = (uint64_t)(row0 + row);
         float inv = 0.0f;
         if constexpr (OUT_FP8) {
-          const float amax = fmaxf(amaxes[row * 2], amaxes[row * 2 + 1]);
-          inv = amax > 0.0f ? 448.0f / amax : 0.0f;
-          if (wn == 0 && hi == 0)
-            P.out_scales[orow * (P.n / 128) + col0 / 128] = amax > 0.0f ? amax / 448.0f : 0.0f;
+          const BlockScale s = block_scale(fmaxf(amaxes[row * 2], amaxes[row * 2 + 1]));
+          inv = s.inv;
+          if (wn == 0 && hi == 0) P.out_scales[orow * (P.n / 128) + col0 / 128] = s.scale;
         }
 #pragma unroll
         for (int f = 0; f < F; ++f) {

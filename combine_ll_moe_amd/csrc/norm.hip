@@ -4,7 +4,8 @@
 // Mathematics, for one row in fp32: h = x + residual; residual_out = h
 // rounded to bf16; y = h / sqrt(mean(h^2) + eps) * weight, taken from h
 // before that rounding; out = y in bf16, or codes e4m3(y * (448 / amax)) and
-// scales amax / 448 of each 128 columns, as the fp8 dispatch quantizes.
+// scales amax / 448 of each 128 columns, as the fp8 dispatch quantizes (tiny
+// blocks apart: block_scale).
 //
 // Design: one workgroup a row (one wavefront for short rows, four rows a
 // workgroup), the row in registers from its one read to its one write: the
@@ -115,13 +116,12 @@ __global__ void __launch_bounds__(ROW < 256 ? 256 : ROW) norm_kernel(const NormP
       for (int j = 0; j < 8; ++j) amax = fmaxf(amax, fabsf(y[j]));  // NaN is ignored
 #pragma unroll
       for (int d = 1; d < 16; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
-      const float inv = amax > 0.0f ? 448.0f / amax : 0.0f;
+      const auto [unit, inv] = block_scale(amax);
       if (in) {
         reinterpret_cast<uint2*>(P.out)[base + i] =
             make_uint2(e4m3_pack4(y[0] * inv, y[1] * inv, y[2] * inv, y[3] * inv),
                        e4m3_pack4(y[4] * inv, y[5] * inv, y[6] * inv, y[7] * inv));
-        if ((i & 15) == 0)
-          P.out_scales[(base + i) / 16] = amax > 0.0f ? amax / 448.0f : 0.0f;
+        if ((i & 15) == 0) P.out_scales[(base + i) / 16] = unit;
       }
     } else if (in) {
       reinterpret_cast<v4u*>(P.out)[base + i] = pack8(y);

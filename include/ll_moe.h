@@ -382,8 +382,9 @@ int ll_moe_clean_signals(void* layout, int max_tokens, int hidden,
  *               LL_MOE_FP8_E4M3 (fp8 with ACT_SILU_MUL only, n % 128 == 0):
  *               per row and 128 columns of the fp32 values, quantized as the
  *               fp8 dispatch does (amax without NaN; codes of v * (448 /
- *               amax); scale amax / 448; 0 and 0 when amax is 0). These are
- *               the a and a_scales of a second product.
+ *               amax); scale amax / 448; 0 and 0 when amax is 0), but where
+ *               amax / 448 < 2^-127 the scale is 2^-127 and the codes are of
+ *               v * 2^127. These are the a and a_scales of a second product.
  *   a:          device [num_experts * max_tokens, k], 16-byte aligned.
  *   a_scales:   device fp32 [num_experts * max_tokens, k / 128] (fp8 only).
  *   w:          device [num_experts, n or 2n, k], 16-byte aligned.
@@ -432,8 +433,8 @@ int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_experts, int gro
  * eps) * weight, from h before that rounding; out = y.
  *   x_dtype:      LL_MOE_BF16, or LL_MOE_FP32 (ll_moe_combine's output).
  *   out_dtype:    LL_MOE_BF16 (what the dispatch takes), or LL_MOE_FP8_E4M3:
- *                 codes and scales as the fp8 dispatch quantizes, from the
- *                 fp32 y (hidden % 128 == 0).
+ *                 codes and scales as ll_moe_expert_gemm's, from the fp32 y
+ *                 (hidden % 128 == 0).
  *   x, residual, residual_out, out: device [num_tokens, hidden], 16-byte
  *                 aligned; residual and residual_out bf16, either may be NULL.
  *   weight:       device bf16 [hidden], 16-byte aligned.
