@@ -26,10 +26,14 @@ MAX_TOPK = 16
 MAX_MESSAGE_BYTES = 45056
 MAX_EXPERTS = 1 << 20
 SEND_MAX_EXPERTS = 4096
-FP32 = 2  # ll_moe_rms_norm: x in fp32
+FP32 = 2  # where a call takes or gives fp32
 ACT_NONE = 0
 ACT_SILU_MUL = 1
 GEMM_MAX_COLUMNS = 1 << 20
+SCORE_SOFTMAX = 0
+SCORE_SIGMOID = 1
+ROUTE_MAX_GROUPS = 64
+DENSE_WORKSPACE = 64 << 20
 REFUSAL_FLAG_WAIT = 1
 REFUSAL_COUNT_WAIT = 2
 RECV_READY = 0x100
@@ -70,6 +74,9 @@ _lib.ll_moe_clean_signals.argtypes = [_vp, _i, _i, _i, _i, _i, _vp]
 _lib.ll_moe_expert_gemm.argtypes = [_i] * 7 + [_vp] * 8
 _lib.ll_moe_expert_gemm_w4.argtypes = [_i] * 6 + [_vp] * 7
 _lib.ll_moe_rms_norm.argtypes = [_i] * 4 + [ctypes.c_float] + [_vp] * 7
+_lib.ll_moe_gate.argtypes = [_i] * 4 + [_vp] * 4
+_lib.ll_moe_route.argtypes = [_i] * 9 + [ctypes.c_float] + [_vp] * 6
+_lib.ll_moe_dense_gemm.argtypes = [_i] * 5 + [_vp] * 9
 _lib.ll_moe_diag_e4m3.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
 _lib.ll_moe_diag_e4m3_in_range.argtypes = [_vp, _vp, ctypes.c_size_t, _vp]
 _lib.ll_moe_diag_watch.argtypes = [_vp, _i, _i, _i, _i, _i, _i, _i, _vp, _vp, _i, _vp, _vp]
@@ -81,6 +88,7 @@ _lib.ll_moe_status_string.restype = ctypes.c_char_p
 for _f in ("ll_moe_layout_bytes", "ll_moe_layout_offsets", "ll_moe_dispatch",
            "ll_moe_combine", "ll_moe_combine_send", "ll_moe_combine_recv", "ll_moe_dispatch_recv",
            "ll_moe_expert_gemm", "ll_moe_expert_gemm_w4", "ll_moe_rms_norm",
+           "ll_moe_gate", "ll_moe_route", "ll_moe_dense_gemm",
            "ll_moe_clean_signals", "ll_moe_diag_e4m3", "ll_moe_diag_e4m3_in_range",
            "ll_moe_diag_watch", "ll_moe_diag_stream",
            "ll_moe_diag_store_rows", "ll_moe_diag_gather_rows"):
@@ -261,6 +269,55 @@ def ll_moe_rms_norm(num_tokens: int, hidden: int, x_dtype: int, out_dtype: int, 
                                 *_operands("ll_moe_rms_norm", stream, x, residual, weight,
                                            residual_out, out, out_scales, items=items, sizes=sizes)),
            "ll_moe_rms_norm")
+
+
+def ll_moe_gate(num_tokens: int, hidden: int, num_experts: int, weight_dtype: int, x, weight,
+                logits, stream=None) -> None:
+    """The router's logits. Tensors are contiguous, on the current device, of
+    the operand's element size and at least as large."""
+    item = 4 if weight_dtype == FP32 else 2
+    sizes = (2 * num_tokens * hidden, item * num_experts * hidden, 4 * num_tokens * num_experts)
+    _check(_lib.ll_moe_gate(num_tokens, hidden, num_experts, weight_dtype,
+                            *_operands("ll_moe_gate", stream, x, weight, logits,
+                                       items=(2, item, 4), sizes=sizes)),
+           "ll_moe_gate")
+
+
+def ll_moe_route(num_tokens: int, num_experts: int, topk: int, logits_dtype: int, score: int,
+                 num_groups: int, topk_groups: int, group_best: int, renormalize: bool,
+                 scale: float, logits, bias, num_valid, topk_idx, topk_weights,
+                 stream=None) -> None:
+    """From logits to picked experts and their weights (bias and num_valid may
+    be None). Tensors are contiguous, on the current device, of the operand's
+    element size and at least as large."""
+    item = 4 if logits_dtype == FP32 else 2
+    picks = 4 * num_tokens * topk
+    _check(_lib.ll_moe_route(num_tokens, num_experts, topk, logits_dtype, score, num_groups,
+                             topk_groups, group_best, renormalize, scale,
+                             *_operands("ll_moe_route", stream, logits, bias, num_valid, topk_idx,
+                                        topk_weights, items=(item, 4, 4, 4, 4),
+                                        sizes=(item * num_tokens * num_experts, 4 * num_experts, 4,
+                                               picks, picks))),
+           "ll_moe_route")
+
+
+def ll_moe_dense_gemm(num_tokens: int, n: int, k: int, act: int, out_dtype: int, a, a_scales, w,
+                      w_scales, addend, out, out_scales, workspace, stream=None) -> None:
+    """Every row through one weight in block-scaled fp8, plain (with an addend,
+    or None) or gated; workspace: DENSE_WORKSPACE bytes. Tensors are
+    contiguous, on the current device, of the operand's element size and at
+    least as large."""
+    rows_w, kb, values = 2 * n if act else n, k // 128, num_tokens * n
+    fp8_out = out_dtype == FP8_E4M3
+    out_item = 1 if fp8_out else 4 if out_dtype == FP32 else 2
+    items = (1, 4, 1, 4, 4, out_item, 4 if fp8_out else 0, 0)
+    sizes = (num_tokens * k, 4 * num_tokens * kb, rows_w * k, 4 * ((rows_w + 127) // 128) * kb,
+             4 * values, out_item * values, values // 32 if fp8_out else 0, DENSE_WORKSPACE)
+    _check(_lib.ll_moe_dense_gemm(num_tokens, n, k, act, out_dtype,
+                                  *_operands("ll_moe_dense_gemm", stream, a, a_scales, w, w_scales,
+                                             addend, out, out_scales, workspace, items=items,
+                                             sizes=sizes)),
+           "ll_moe_dense_gemm")
 
 
 def ll_moe_clean_signals(layout, max_tokens: int, hidden: int, num_experts: int, dtype: int,

@@ -14,7 +14,7 @@ CSRC = os.path.join(HERE, "csrc")
 LIB = os.path.join(HERE, "libllmoe.so")
 SOURCES = ["gemm_few_int4.hip", "gemm_tile.hip", "gemm_few_fp8.hip", "gemm_few_bf16.hip",  # longest first
            "api.hip", "dispatch.hip", "combine.hip", "two_phase.hip", "receive.hip", "watch.hip",
-           "probe.hip", "expert_api.hip", "norm.hip"]
+           "probe.hip", "expert_api.hip", "norm.hip", "dense.hip", "pick.hip", "gate.hip", "layer_api.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -362,7 +362,7 @@ int ll_moe_clean_signals(void* layout, int max_tokens, int hidden,
  * calls may run at once on several streams. All may be captured; a replay
  * reads the counts as they are then.
  */
-#define LL_MOE_FP32 2                /* ll_moe_rms_norm: x in fp32 */
+#define LL_MOE_FP32 2                /* where a call takes or gives fp32 */
 #define LL_MOE_ACT_NONE 0
 #define LL_MOE_ACT_SILU_MUL 1        /* silu(gate) * up */
 #define LL_MOE_GEMM_MAX_COLUMNS (1 << 20)
@@ -447,6 +447,111 @@ int ll_moe_expert_gemm_w4(int max_tokens, int n, int k, int num_experts, int gro
 int ll_moe_rms_norm(int num_tokens, int hidden, int x_dtype, int out_dtype, float eps,
                     const void* x, const void* residual, const void* weight,
                     void* residual_out, void* out, float* out_scales, hipStream_t stream);
+
+/*
+ * The router and the dense products: what a layer computes of every token
+ * beside its routed experts. The router gives the dispatch its topk_idx and
+ * the combine its topk_weights; a shared expert (or a dense layer) is two
+ * products whose result joins the combine's. As above, no page defines these,
+ * calls enqueue one or two kernels, may be captured, and the same call gives
+ * the same bits.
+ */
+
+/*
+ * ll_moe_gate - the router's logits.
+ *   logits[t, e] = sum over c < hidden of x[t, c] * weight[e, c]
+ * with exact products and fp32 sums (fp32 weights are not rounded).
+ *   weight_dtype: LL_MOE_BF16 or LL_MOE_FP32.
+ *   x:       device bf16 [num_tokens, hidden], 16-byte aligned.
+ *   weight:  device [num_experts, hidden], 16-byte aligned.
+ *   logits:  device fp32 [num_tokens, num_experts], 16-byte aligned.
+ *   num_tokens >= 0 (0 enqueues nothing), hidden % 8 == 0, hidden <= 32768,
+ *   num_experts <= 4096. logits may overlap neither input. A token's logits
+ * are of its row and the weights alone (a NaN stays in its row); how a sum is
+ * grouped goes by the sizes of the call. With fp32 weights an infinity in x,
+ * or a weight that is not finite, gives NaN. Enqueued on `stream`.
+ */
+int ll_moe_gate(int num_tokens, int hidden, int num_experts, int weight_dtype, const void* x,
+                const void* weight, float* logits, hipStream_t stream);
+
+/*
+ * ll_moe_route - from logits to picked experts and their weights.
+ * For every row t, in 64 bits,
+ *   s[e] = 1 / (1 + exp(-l[e])) (LL_MOE_SCORE_SIGMOID), or
+ *          exp(l[e]) / sum over j of exp(l[j]) (LL_MOE_SCORE_SOFTMAX)
+ *   v[e] = s[e] + bias[e]; without a bias the order of v is that of l
+ *   groups (num_groups > 1): num_groups equal runs of experts; a group's value
+ *          is the sum of its group_best (1 or 2) largest v; the topk_groups
+ *          groups of the largest values stay, of equal ones the first
+ *   topk_idx[t, k]: the topk largest v of the groups that stay, in descending
+ *          order, of equal ones the first
+ *   topk_weights[t, k] = scale * s[e], or with renormalize
+ *          scale * s[e] / sum over the row's picks of s; fp32, rounded once.
+ * A logit that is NaN or -infinity leaves its expert out, of the picks and of
+ * the softmax's sum; so does a bias that is, of the picks. A group that has
+ * fewer than group_best experts left counts as -infinity. +infinity counts as
+ * the largest fp32 (3.4e38). Where fewer than topk experts are left, the picks behind them are
+ * -1 with weight 0, as are all picks of rows at or behind *num_valid: the
+ * dispatch and the combine leave such entries out. Renormalised weights are
+ * right where every picked score underflows, too.
+ *   logits_dtype: LL_MOE_FP32 or LL_MOE_BF16.
+ *   logits:       device [num_tokens, num_experts], 16-byte aligned; rows
+ *                 behind *num_valid are not read.
+ *   bias:         device fp32 [num_experts], or NULL.
+ *   num_valid:    device int32, or NULL: every row is valid. Read when the
+ *                 call runs, so a captured call serves batches of any size.
+ *   topk_idx:     device int32 [num_tokens, topk].
+ *   topk_weights: device fp32 [num_tokens, topk].
+ *   num_tokens >= 0 (0 enqueues nothing), num_experts <= 4096, topk <=
+ *   LL_MOE_MAX_TOPK, num_tokens * topk < 2^31, num_groups <= 64 and a divisor
+ *   of num_experts, topk <= topk_groups * (num_experts / num_groups),
+ *   group_best <= num_experts / num_groups if there are groups, renormalize 0
+ *   or 1, scale finite. Outputs may overlap neither an input nor each other.
+ * Enqueued on `stream`.
+ */
+#define LL_MOE_SCORE_SOFTMAX 0
+#define LL_MOE_SCORE_SIGMOID 1
+#define LL_MOE_ROUTE_MAX_GROUPS 64
+int ll_moe_route(int num_tokens, int num_experts, int topk, int logits_dtype, int score,
+                 int num_groups, int topk_groups, int group_best, int renormalize, float scale,
+                 const void* logits, const float* bias, const int32_t* num_valid,
+                 int32_t* topk_idx, float* topk_weights, hipStream_t stream);
+
+/*
+ * ll_moe_dense_gemm - every row through one weight, in block-scaled fp8: a
+ * shared expert's products, or a dense layer's.
+ *   P[r, i] = sum over c < k of A[r, c] * W[i, c], in fp32, with
+ *   A[r, c] = code * a_scales[r, c / 128], W[i, c] = code * w_scales[i / 128, c / 128]
+ *   ACT_NONE:     out[r, i] = P[r, i] + addend[r, i] (no addend: P), i < n;
+ *                 out_dtype LL_MOE_BF16 or LL_MOE_FP32.
+ *   ACT_SILU_MUL: out[r, i] = g / (1 + exp(-g)) * u with g = P[r, i],
+ *                 u = P[r, n + i] (W has n gate rows, then n up rows);
+ *                 out_dtype LL_MOE_BF16 or LL_MOE_FP8_E4M3 (n % 128 == 0,
+ *                 codes and scales as ll_moe_expert_gemm's). No addend.
+ *   a:          device e4m3 [num_tokens, k], 16-byte aligned.
+ *   a_scales:   device fp32 [num_tokens, k / 128].
+ *   w:          device e4m3 [n or 2n, k], 16-byte aligned.
+ *   w_scales:   device fp32 [ceil(rows of W / 128), k / 128].
+ *   addend:     device fp32 [num_tokens, n], 16-byte aligned, or NULL: what
+ *               the product joins, such as ll_moe_combine's output. May be
+ *               out itself if out is fp32.
+ *   out:        device [num_tokens, n], 16-byte aligned.
+ *   out_scales: device fp32 [num_tokens, n / 128] (fp8 out).
+ *   workspace:  device, LL_MOE_DENSE_WORKSPACE bytes, 16-byte aligned, for
+ *               partial sums. What it holds before does not matter, what it
+ *               holds after is unspecified. Calls that may run at the same
+ *               time need one each (two graphs that may run at once, too).
+ *   num_tokens >= 0 (0 enqueues nothing), k % 128 == 0, n % 16 == 0, both <=
+ *   LL_MOE_GEMM_MAX_COLUMNS. Apart from the addend, outputs and the workspace
+ *   may overlap neither an input nor each other. A row's products are of that
+ *   row and the weights alone; how its sum is grouped goes by the sizes of the
+ *   call. Enqueued on `stream`.
+ */
+#define LL_MOE_DENSE_WORKSPACE (64 << 20)
+int ll_moe_dense_gemm(int num_tokens, int n, int k, int act, int out_dtype, const void* a,
+                      const float* a_scales, const void* w, const float* w_scales,
+                      const float* addend, void* out, float* out_scales, void* workspace,
+                      hipStream_t stream);
 
 /* Name of a status code (static string). */
 const char* ll_moe_status_string(int status);
