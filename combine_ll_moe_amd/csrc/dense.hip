@@ -17,47 +17,45 @@
 #include <stdint.h>
 
 #include "dense.h"
-#include "expert_gemm.h"
-#include "kernels.h"
+#include "layout.h"
+#include "ll_moe.h"
+#include "tile.h"
 
 namespace llmoe {
 namespace {
 
-typedef __attribute__((address_space(3))) uint8_t LdsByte;
-
 enum : int { kPartial = 0, kPlain = 1, kGated = 2, kGatedFp8 = 3 };
-constexpr int kStep = 128;  // bytes and columns of a k step
+static_assert(kStep == kFp8Block);  // a k step is one scale's columns
+constexpr int64_t kWorkspace = LL_MOE_DENSE_WORKSPACE;
+// Rows up to which a tile has 16, 64 and 128 of them, and steps of k that a
+// split has to save, to be worth its second kernel.
+constexpr int kFewTokens = 32, kSomeTokens = 256, kSomeGatedTokens = 128, kManyTokens = 4096;
+constexpr int kWorthSplit = 12;
 
-// s_waitcnt vmcnt(n) alone.
-template <int N>
-__device__ __forceinline__ void wait_loads() {
-  __builtin_amdgcn_s_waitcnt(0x0F70 | (N & 15) | (N >> 4) << 14);
-}
-
-// What workgroup b of `total` does: the XCDs, to which workgroups are dealt
-// in turn, take runs of the tiles, in which neighbours share rows or weights.
-__device__ __forceinline__ uint32_t run_of_xcd(uint32_t b, uint32_t total) {
-  const uint32_t x = b % kXcds, whole = total / kXcds, more = total % kXcds;
-  return x * whole + (x < more ? x : more) + b / kXcds;
-}
-
-// WM x WN wavefronts, each FM x FN fragments of 16 x 16.
+// WM x WN wavefronts, each FM x FN fragments of 16 x 16; STAGES buffers of a
+// step in LDS. The steps of k are divided among `splits` workgroups.
 template <int WM, int WN, int FM, int FN, int STAGES, int MODE>
-__global__ void __launch_bounds__(WM* WN * 64) dense_kernel(const DenseParams P, int splits) {
+__global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams P, int splits) {
   constexpr int BM = WM * FM * 16, BN = WN * FN * 16, WAVES = WM * WN;
   constexpr bool GATED = MODE == kGated || MODE == kGatedFp8;
   constexpr int COLS = GATED ? BN / 2 : BN;  // output columns of a tile
   constexpr int AI = BM / 8, WI = BN / 8;    // copies of 8 rows
-  constexpr int STAGE = (BM + BN) * kStep;
-  static_assert(STAGES == 2 || STAGES == 4);
-  static_assert(WI % WAVES == 0 && (!GATED || WI / 2 % WAVES == 0));
+  constexpr int AC = (AI + WAVES - 1) / WAVES, WC = WI / WAVES;  // of a wavefront
+  constexpr int SCALES = (BM + BN) * kStep;  // in a stage: 512 bytes of scales a wavefront
+  constexpr int STAGE = SCALES + WAVES * 512;
+  static_assert(FM <= 4);
+  static_assert(STAGES >= 2 && STAGES <= 6);
+  static_assert(WI % WAVES == 0 && (AI % WAVES == 0 || WAVES % AI == 0) && (!GATED || WI / 2 % WAVES == 0));
   static_assert(FN * 16 <= 128 && (MODE != kGatedFp8 || BN == 256));
+  // an array each, so that the compiler can tell a step's copies from the
+  // reads of another one's
   __shared__ __align__(16) uint8_t st0[STAGE], st1[STAGE];
-  __shared__ __align__(16) uint8_t st2[STAGES > 2 ? STAGE : 16], st3[STAGES > 2 ? STAGE : 16];
+  __shared__ __align__(16) uint8_t st2[STAGES > 2 ? STAGE : 16], st3[STAGES > 3 ? STAGE : 16];
+  __shared__ __align__(16) uint8_t st4[STAGES > 4 ? STAGE : 16], st5[STAGES > 5 ? STAGE : 16];
   const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
-  const int rows_w = GATED || (MODE == kPartial && P.gated) ? 2 * P.n : P.n;
+  const int rows_w = P.gated ? 2 * P.n : P.n;
   const int width = GATED ? P.n : rows_w;  // columns that the tiles cover
   const uint32_t ld = (uint32_t)P.k;
   const int kb = P.k / 128;
@@ -77,49 +75,44 @@ __global__ void __launch_bounds__(WM* WN * 64) dense_kernel(const DenseParams P,
   const Rsrc ra = rsrc_of(P.a + (uint64_t)row0 * ld, (uint32_t)rows * ld);
   const Rsrc rw = rsrc_of(P.w + (uint64_t)col0 * ld, (uint32_t)cols * ld);
   const Rsrc ru = rsrc_of(P.w + (uint64_t)(GATED ? P.n + col0 : 0) * ld, GATED ? (uint32_t)cols * ld : 0u);
-  const uint32_t sub = (uint32_t)lane >> 3, chunk = (uint32_t)((lane & 7) ^ sub) * 16;
-  auto copy = [&](int step, uint8_t* lds) __attribute__((always_inline)) {
-    const uint32_t from = (uint32_t)step * kStep + chunk;
-    const bool in = step < k1;
-#pragma unroll
-    for (int i = 0; i < (AI + WAVES - 1) / WAVES; ++i) {
-      const int g = i * WAVES + wave;
-      if (AI % WAVES == 0 || g < AI)
-        __builtin_amdgcn_raw_ptr_buffer_load_lds(ra, (LdsByte*)(lds + g * 8 * kStep), 16,
-                                                 in ? (int)((g * 8 + sub) * ld + from) : (int)kOutside, 0, 0, 0);
-    }
-#pragma unroll
-    for (int i = 0; i < WI / WAVES; ++i) {
-      const bool up = GATED && i >= WI / 2 / WAVES;
-      const int g = i * WAVES + wave, r = up ? g - WI / 2 : g;
-      __builtin_amdgcn_raw_ptr_buffer_load_lds(up ? ru : rw, (LdsByte*)(lds + (BM + g * 8) * kStep), 16,
-                                               in ? (int)((r * 8 + sub) * ld + from) : (int)kOutside, 0, 0, 0);
-    }
-  };
-
-  // scales of a step: this lane's rows, and the weight blocks of this
-  // wavefront's fragments. Its plain columns lie in one block; gated, its gate
-  // columns do, and its up rows, which start at any multiple of 16, lie in the
-  // next one from fragment `edge` on.
+  const uint32_t sub = (uint32_t)lane >> 3, mine = sub * ld + ((lane & 7) ^ sub) * 16;
+  // Scales of a step: of this wavefront's rows, a lane each, and of the weight
+  // blocks of its fragments, in lanes 0 to 2. Its plain columns lie in one
+  // block; gated, its gate columns do, and its up rows, which start at any
+  // multiple of 16, lie in the next one from fragment `edge` on.
   const Rsrc ras = rsrc_of(P.a_scales + (uint64_t)row0 * kb, (uint32_t)rows * kb * 4u);
-  const int first = GATED ? col0 + wn * (FN * 8) : col0 + wn * (FN * 16);
-  const int first_up = P.n + col0 + wn * (FN * 8);
   const int last = (rows_w + 127) / 128 - 1;
-  const int b0 = first / 128 < last ? first / 128 : last;
-  const int b1 = first_up / 128 < last ? first_up / 128 : last, b2 = b1 < last ? b1 + 1 : last;
+  const int first = GATED ? col0 + wn * (FN * 8) : col0 + wn * (FN * 16);
+  const int first_up = P.n + first;
   const int edge = ((first_up / 128 + 1) * 128 - first_up) / 16;
-  float as[2][FM], ws[2][3];
-  auto scales = [&](int step, float (&av)[FM], float (&wv)[3]) __attribute__((always_inline)) {
-    const int s = step < kb ? step : kb - 1;
+  const int block = !GATED || lane == 0 ? first / 128 : first_up / 128 + (lane > 1);
+  const Rsrc rws = rsrc_of(P.w_scales, (uint32_t)(last + 1) * kb * 4u);
+  const uint32_t my_row = 4u * (uint32_t)((wm * FM * 16 + (lane & (FM * 16 - 1))) * kb);
+  const uint32_t my_block = 4u * (uint32_t)((block < last ? block : last) * kb);
+
+  // Everything of a step: the copies into its buffer, and its scales. Every
+  // wavefront issues the same number of loads, steps behind k1 too (those read
+  // nothing): the waits count them.
+  constexpr int LOADS = AC + WC + 2;
+  auto fetch = [&](int step, uint8_t* lds) __attribute__((always_inline)) {
+    // offsets: the lane's own and a uniform part, which is outside every
+    // descriptor behind k1
+    const uint32_t at = step < k1 ? (uint32_t)step * kStep : kOutside;
 #pragma unroll
-    for (int f = 0; f < FM; ++f)
-      av[f] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(
-          ras, (int)(4u * ((uint32_t)(wm * FM * 16 + f * 16 + lo) * kb + s)), 0, 0));
-    wv[0] = P.w_scales[(int64_t)b0 * kb + s];
-    if constexpr (GATED) {
-      wv[1] = P.w_scales[(int64_t)b1 * kb + s];
-      wv[2] = P.w_scales[(int64_t)b2 * kb + s];
+    for (int i = 0; i < AC; ++i) {
+      const int g = AI < WAVES ? wave % AI : i * WAVES + wave;
+      copy16(ra, lds + g * 8 * kStep, mine + (g * 8 * ld + at));
     }
+#pragma unroll
+    for (int i = 0; i < WC; ++i) {
+      const bool up = GATED && i >= WC / 2;
+      const int g = i * WAVES + wave, r = up ? g - WI / 2 : g;
+      copy16(up ? ru : rw, lds + (BM + g * 8) * kStep, mine + (r * 8 * ld + at));
+    }
+    const uint32_t s = step < k1 ? 4u * (uint32_t)step : kOutside;
+    uint8_t* scales = lds + SCALES + wave * 512;
+    copy4(ras, scales, my_row + s);
+    copy4(rws, scales + 256, my_block + s);
   };
 
   // LDS row of weight fragment f: gated, fragments from FN / 2 on are the up
@@ -138,7 +131,12 @@ __global__ void __launch_bounds__(WM* WN * 64) dense_kernel(const DenseParams P,
   for (int m = 0; m < FM; ++m)
 #pragma unroll
     for (int f = 0; f < FN; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
-  auto multiply = [&](const uint8_t* lds, const float (&av)[FM], const float (&wv)[3]) __attribute__((always_inline)) {
+  auto multiply = [&](const uint8_t* lds) __attribute__((always_inline)) {
+    const float* scales = reinterpret_cast<const float*>(lds + SCALES + wave * 512);
+    float av[FM];
+#pragma unroll
+    for (int m = 0; m < FM; ++m) av[m] = scales[m * 16 + lo];
+    const float w0 = scales[64], w1 = GATED ? scales[65] : 0.0f, w2 = GATED ? scales[66] : 0.0f;
     Bf16x16 a[FM][2];
 #pragma unroll
     for (int m = 0; m < FM; ++m)
@@ -157,31 +155,29 @@ __global__ void __launch_bounds__(WM* WN * 64) dense_kernel(const DenseParams P,
           p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j].lo, a[m][j].lo, p, 0, 0, 0);
           p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j].hi, a[m][j].hi, p, 0, 0, 0);
         }
-        const float sc = av[m] * wv[!GATED || f < FN / 2 ? 0 : f - FN / 2 < edge ? 1 : 2];
+        const float sc = av[m] * (!GATED || f < FN / 2 ? w0 : f - FN / 2 < edge ? w1 : w2);
 #pragma unroll
         for (int r = 0; r < 4; ++r) acc[m][f][r] = __builtin_fmaf(sc, p[r], acc[m][f][r]);
       }
     }
   };
 
-  // A step's copies are waited for, then all wavefronts meet: the step is
-  // whole, and the buffer of the one before it free for the copies of the
-  // step STAGES - 1 ahead. Only the copies of the steps between may be under way.
+  // A step's loads are waited for, those of the steps behind it still under
+  // way, then all wavefronts meet: the step is whole, and the buffer of the one
+  // before it is free for the step STAGES - 1 ahead.
   constexpr int AHEAD = STAGES - 1;
-  uint8_t* const buffers[4] = {st0, st1, st2, st3};
+  uint8_t* const buffers[6] = {st0, st1, st2, st3, st4, st5};
 #pragma unroll
-  for (int s = 0; s < AHEAD; ++s) copy(k0 + s, buffers[s]);
-  scales(k0, as[0], ws[0]);
+  for (int s = 0; s < AHEAD; ++s) fetch(k0 + s, buffers[s]);
+  // Steps behind k1 are zeros: whole rounds of STAGES, without branches.
   for (int k = k0; k < k1; k += STAGES) {
 #pragma unroll
     for (int s = 0; s < STAGES; ++s) {
-      if (k + s < k1) {
-        wait_loads<0>();
-        __syncthreads();
-        copy(k + s + AHEAD, buffers[(s + AHEAD) % STAGES]);
-        scales(k + s + 1, as[(s + 1) & 1], ws[(s + 1) & 1]);
-        multiply(buffers[s], as[s & 1], ws[s & 1]);
-      }
+      wait_loads<(AHEAD - 1) * LOADS>();
+      meet();
+      fetch(k + s + AHEAD, buffers[(s + AHEAD) % STAGES]);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(buffers[s]);
     }
   }
 
@@ -246,6 +242,60 @@ __global__ void __launch_bounds__(WM* WN * 64) dense_kernel(const DenseParams P,
   }
 }
 
+// The partial sums of `splits` runs of k to outputs: a thread has four columns
+// of a row, 32 of them a block of 128 columns.
+__global__ void __launch_bounds__(256) dense_finish_kernel(const DenseParams P, int splits) {
+  const int blocks = (P.n + 127) / 128;
+  const int64_t item = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int64_t row = item / 32 / blocks;
+  const int col = (int)(item / 32 % blocks) * 128 + (int)(item & 31) * 4;
+  const int width = P.gated ? 2 * P.n : P.n;
+  const bool in = row < P.m && col < P.n;
+  f32x4 v = {0, 0, 0, 0}, u = {0, 0, 0, 0};
+  if (in) {
+    const float* at = P.partial + row * width + col;
+    for (int s = 0; s < splits; ++s) {
+      v += *reinterpret_cast<const f32x4*>(at);
+      if (P.gated) u += *reinterpret_cast<const f32x4*>(at + P.n);
+      at += (int64_t)P.m * width;
+    }
+  }
+  if (P.gated)
+#pragma unroll
+    for (int q = 0; q < 4; ++q) v[q] = silu_mul(v[q], u[q]);
+  const uint64_t to = (uint64_t)row * P.n + col;
+  if (P.out_type == kOutFp8) {
+    float amax = fmaxf(fmaxf(fabsf(v[0]), fabsf(v[1])), fmaxf(fabsf(v[2]), fabsf(v[3])));  // NaN is ignored
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) amax = fmaxf(amax, __shfl_xor(amax, d, 64));
+    const BlockScale s = block_scale(amax);
+    if (!in) return;
+    *reinterpret_cast<uint32_t*>(P.out + to) = e4m3_pack4(v[0] * s.inv, v[1] * s.inv, v[2] * s.inv, v[3] * s.inv);
+    if ((item & 31) == 0) P.out_scales[row * blocks + col / 128] = s.scale;
+    return;
+  }
+  if (!in) return;
+  if (P.addend) v += *reinterpret_cast<const f32x4*>(P.addend + to);
+  if (P.out_type == kOutFp32)
+    *reinterpret_cast<f32x4*>(P.out + 4 * to) = v;
+  else
+    *reinterpret_cast<uint2*>(P.out + 2 * to) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
+}
+
+// Through partial sums in the workspace, which they fit.
+template <int WM, int WN, int FM, int FN, int STAGES>
+hipError_t launch_split(const DenseParams& p, int splits, hipStream_t stream) {
+  constexpr int BM = WM * FM * 16, BN = WN * FN * 16;
+  const int64_t width = p.gated ? 2 * (int64_t)p.n : p.n;
+  const int64_t tiles = (width + BN - 1) / BN * (((int64_t)p.m + BM - 1) / BM) * splits;
+  dense_kernel<WM, WN, FM, FN, STAGES, kPartial><<<(unsigned)tiles, WM * WN * 64, 0, stream>>>(p, splits);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const int64_t threads = (int64_t)p.m * ((p.n + 127) / 128) * 32;
+  dense_finish_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(p, splits);
+  return hipGetLastError();
+}
+
 // The product of `rows` rows from row `first` on.
 DenseParams rows_from(const DenseParams& p, uint64_t first, int rows) {
   DenseParams q = p;
@@ -279,9 +329,35 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
 
 hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   if (p.m == 0) return hipSuccess;
-  if (!p.gated) return launch<1, 4, 4, 4, 2, kPlain>(p, stream);
-  return p.out_type == kOutFp8 ? launch<1, 4, 4, 4, 2, kGatedFp8>(p, stream)
-                               : launch<1, 4, 4, 4, 2, kGated>(p, stream);
+  const int64_t rows_w = p.gated ? 2 * (int64_t)p.n : p.n, kb = p.k / 128;
+  const int64_t bytes = (int64_t)p.m * rows_w * 4;  // of one set of partial sums
+  // Runs of k for tiles of bm x bn of which `room` are under way at once: as
+  // many as there is room for, of 7 steps or more.
+  auto runs = [&](int64_t bm, int64_t bn, int64_t room) {
+    const int64_t tiles = (rows_w + bn - 1) / bn * ((p.m + bm - 1) / bm);
+    int64_t s = room / tiles;
+    if (s > kb / 7) s = kb / 7;
+    if (s > kWorkspace / bytes) s = kWorkspace / bytes;
+    return s < 1 ? 1 : s;
+  };
+  if (p.m <= kFewTokens) {
+    const int64_t s = runs(16, 64, 256);
+    if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<1, 4, 1, 1, 4>(p, (int)s, stream);
+    return launch<1, 4, 1, 1, 4, kPlain>(p, stream);
+  }
+  if (p.m <= (p.gated ? kSomeGatedTokens : kSomeTokens)) {
+    const int64_t s = runs(64, 64, 256);
+    if ((p.gated && bytes <= kWorkspace) || kb - kb / s >= kWorthSplit)
+      return launch_split<2, 2, 2, 2, 4>(p, (int)s, stream);
+    if (!p.gated) return launch<2, 2, 2, 2, 4, kPlain>(p, stream);
+  }
+  if (bytes <= kWorkspace && p.m <= kManyTokens) {
+    const int64_t s = runs(128, 128, 512);
+    if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<2, 2, 4, 4, 2>(p, (int)s, stream);
+  }
+  if (!p.gated) return launch<2, 2, 4, 4, 2, kPlain>(p, stream);
+  return p.out_type == kOutFp8 ? launch<4, 2, 4, 8, 2, kGatedFp8>(p, stream)
+                               : launch<4, 2, 4, 8, 2, kGated>(p, stream);
 }
 
 }  // namespace llmoe

@@ -13,14 +13,15 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
-#include "expert_gemm.h"
 #include "gate.h"
+#include "tile.h"
 
 namespace llmoe {
 namespace {
 
 constexpr int kWaves = 8;
 constexpr int kColumns = 64;  // of a step
+constexpr int64_t kFewLogits = 1 << 18, kManyTiles = 192;
 
 __device__ __forceinline__ uint32_t opaque_zero() {
   uint32_t zero = 0;
@@ -154,15 +155,167 @@ __global__ void __launch_bounds__(kWaves * 64) gate_few_kernel(const GateParams 
   }
 }
 
-}  // namespace
+// Many tokens: tiles of BM tokens x BN experts on WM x WN wavefronts, each FM
+// x FN fragments; a step of 64 columns is copied straight into LDS, STAGES - 1
+// steps ahead of the products.
+template <bool FP32, int WM, int WN, int FM, int FN, int STAGES>
+__global__ void __launch_bounds__(WM* WN * 64, 2) gate_tile_kernel(const GateParams P) {
+  constexpr int BM = WM * FM * 16, BN = WN * FN * 16, WAVES = WM * WN;
+  constexpr int ITEM = FP32 ? 4 : 2, WROW = kColumns * ITEM, CH = WROW / 16;
+  constexpr int STAGE = BM * kStep + BN * WROW;
+  constexpr int XC = BM / 8 / WAVES, WC = BN * WROW / 1024 / WAVES, LOADS = XC + WC;
+  static_assert(STAGES >= 2 && STAGES <= 4 && BM / 8 % WAVES == 0 && BN * WROW / 1024 % WAVES == 0);
+  // an array each, so that the compiler can tell a step's copies from the
+  // reads of another one's
+  __shared__ __align__(16) uint8_t st0[STAGE], st1[STAGE];
+  __shared__ __align__(16) uint8_t st2[STAGES > 2 ? STAGE : 16], st3[STAGES > 3 ? STAGE : 16];
+  const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave / WN, wn = wave % WN;
+  const uint32_t ldx = (uint32_t)P.hidden * 2, ldw = (uint32_t)P.hidden * ITEM;
+  const int steps = (P.hidden + kColumns - 1) / kColumns;
+  const uint32_t across = (uint32_t)((P.num_experts + BN - 1) / BN);
+  const uint32_t tile = run_of_xcd(blockIdx.x, gridDim.x);
+  const int e0 = (int)(tile % across) * BN;
+  const int64_t row0 = (int64_t)(tile / across) * BM;
+  const int rows = P.num_tokens - row0 < BM ? (int)(P.num_tokens - row0) : BM;
+  const int experts = P.num_experts - e0 < BN ? P.num_experts - e0 : BN;
+  const Rsrc rx = rsrc_of(P.x + (uint64_t)row0 * ldx, (uint32_t)rows * ldx);
+  const Rsrc rw = rsrc_of(P.w + (uint64_t)e0 * ldw, (uint32_t)experts * ldw);
 
-hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
-  if (p.num_tokens == 0) return hipSuccess;
+  // A row's 16-byte chunks are permuted by the row's low bits, so that the 16
+  // lanes that read one chunk of 16 rows meet no bank twice.
+  const uint32_t xs = (uint32_t)lane >> 3, xc = ((lane & 7) ^ xs) * 16;
+  constexpr int WR = 64 / CH;  // rows of W a copy
+  const uint32_t ws = (uint32_t)lane / CH;
+  auto fetch = [&](int step, uint8_t* lds) __attribute__((always_inline)) {
+    const uint32_t from = (uint32_t)step * kStep + xc;
+    const uint32_t at = step < steps && from < ldx ? xs * ldx + from : kOutside;
+#pragma unroll
+    for (int i = 0; i < XC; ++i) {
+      const uint32_t g = i * WAVES + wave;
+      copy16(rx, lds + g * 8 * kStep, at + g * 8 * ldx);
+    }
+#pragma unroll
+    for (int i = 0; i < WC; ++i) {
+      const uint32_t g = i * WAVES + wave, r = g * WR + ws;
+      const uint32_t wfrom = (uint32_t)step * WROW + ((lane % CH) ^ (r & (CH - 1))) * 16;
+      copy16(rw, lds + BM * kStep + g * 1024, step < steps && wfrom < ldw ? r * ldw + wfrom : kOutside);
+    }
+  };
+  auto x_chunk = [&](const uint8_t* lds, int m, int c) {
+    const int r = wm * FM * 16 + m * 16 + lo;
+    return *reinterpret_cast<const v4u*>(lds + r * kStep + ((c ^ (r & 7)) << 4));
+  };
+  auto w_chunk = [&](const uint8_t* lds, int f, int c) {
+    const int r = wn * FN * 16 + f * 16 + lo;
+    return *reinterpret_cast<const v4u*>(lds + BM * kStep + r * WROW + ((c ^ (r & (CH - 1))) << 4));
+  };
+  f32x4 acc[FM][FN];
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+#pragma unroll
+    for (int f = 0; f < FN; ++f) acc[m][f] = f32x4{0, 0, 0, 0};
+  auto multiply = [&](const uint8_t* lds) __attribute__((always_inline)) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      bf16x8 a[FM];
+#pragma unroll
+      for (int m = 0; m < FM; ++m) a[m] = __builtin_bit_cast(bf16x8, x_chunk(lds, m, 4 * j + hi));
+#pragma unroll
+      for (int f = 0; f < FN; ++f) {
+        if constexpr (FP32) {
+          const Parts w = cut(w_chunk(lds, f, 8 * j + 2 * hi), w_chunk(lds, f, 8 * j + 2 * hi + 1));
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+#pragma unroll
+            for (int m = 0; m < FM; ++m)
+              acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.part[p], a[m], acc[m][f], 0, 0, 0);
+        } else {
+          const bf16x8 w = __builtin_bit_cast(bf16x8, w_chunk(lds, f, 4 * j + hi));
+#pragma unroll
+          for (int m = 0; m < FM; ++m)
+            acc[m][f] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w, a[m], acc[m][f], 0, 0, 0);
+        }
+      }
+    }
+  };
+  constexpr int AHEAD = STAGES - 1;
+  uint8_t* const buffers[4] = {st0, st1, st2, st3};
+#pragma unroll
+  for (int s = 0; s < AHEAD; ++s) fetch(s, buffers[s]);
+  for (int k = 0; k < steps; k += STAGES) {
+#pragma unroll
+    for (int s = 0; s < STAGES; ++s) {
+      wait_loads<(AHEAD - 1) * LOADS>();
+      meet();
+      fetch(k + s + AHEAD, buffers[(s + AHEAD) % STAGES]);
+      __builtin_amdgcn_sched_barrier(0);
+      multiply(buffers[s]);
+    }
+  }
+#pragma unroll
+  for (int m = 0; m < FM; ++m) {
+    const int r = wm * FM * 16 + m * 16 + lo;
+    if (r >= rows) continue;
+#pragma unroll
+    for (int f = 0; f < FN; ++f) {
+      const int e = wn * FN * 16 + f * 16 + 4 * hi;
+      float* to = P.logits + (row0 + r) * P.num_experts + e0 + e;
+      if (P.num_experts % 4 == 0) {
+        if (e < experts) *reinterpret_cast<f32x4*>(to) = acc[m][f];
+      } else {
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          if (e + q < experts) to[q] = acc[m][f][q];
+      }
+    }
+  }
+}
+
+template <bool FP32, int WM, int WN, int FM, int FN, int STAGES>
+hipError_t launch_tile(const GateParams& p, hipStream_t stream) {
+  constexpr int BM = WM * FM * 16, BN = WN * FN * 16, THREADS = WM * WN * 64;
+  const int64_t across = (p.num_experts + BN - 1) / BN;
+  // a grid has fewer than 2^32 threads: more rows go out in several launches
+  const int64_t most = (1ll << 31) / THREADS / across * BM;
+  GateParams q = p;
+  for (int64_t first = 0; first < p.num_tokens; first += most) {
+    q.x = p.x + (uint64_t)first * p.hidden * 2;
+    q.logits = p.logits + first * p.num_experts;
+    q.num_tokens = (int)(p.num_tokens - first < most ? p.num_tokens - first : most);
+    const int64_t tiles = across * ((q.num_tokens + (int64_t)BM - 1) / BM);
+    gate_tile_kernel<FP32, WM, WN, FM, FN, STAGES><<<(unsigned)tiles, THREADS, 0, stream>>>(q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+template <bool FP32>
+hipError_t launch_few(const GateParams& p, hipStream_t stream) {
   const int64_t tiles = (((int64_t)p.num_tokens + 15) / 16) * ((p.num_experts + 15) / 16);
   const unsigned blocks = (unsigned)(tiles < 1 << 16 ? tiles : 1 << 16);
-  if (p.w_fp32) gate_few_kernel<true><<<blocks, kWaves * 64, 0, stream>>>(p);
-  else gate_few_kernel<false><<<blocks, kWaves * 64, 0, stream>>>(p);
+  gate_few_kernel<FP32><<<blocks, kWaves * 64, 0, stream>>>(p);
   return hipGetLastError();
+}
+
+}  // namespace
+
+// Which kernel: the first up to kFewLogits logits (bf16, hidden 7168 and 256
+// experts: 512 tokens 15.5 us against 23.5 in tiles of 64 x 64, 1024 tokens 30
+// against 29; fp32 1024 tokens 55 against 82, 2048 tokens 108 against 82). Then
+// tiles of 64 x 64, and of 128 x 128 where those are kManyTiles or more (4096
+// tokens: 36 us against 68; 16384 tokens: 118 against 80, fp32 257 against 196).
+hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
+  if (p.num_tokens == 0) return hipSuccess;
+  const int64_t logits = (int64_t)p.num_tokens * p.num_experts;
+  if (logits <= (p.w_fp32 ? kFewLogits * 3 / 2 : kFewLogits))
+    return p.w_fp32 ? launch_few<true>(p, stream) : launch_few<false>(p, stream);
+  const int64_t tiles = (((int64_t)p.num_tokens + 127) / 128) * ((p.num_experts + 127) / 128);
+  if (tiles < kManyTiles)
+    return p.w_fp32 ? launch_tile<true, 2, 2, 2, 2, 3>(p, stream) : launch_tile<false, 2, 2, 2, 2, 4>(p, stream);
+  return p.w_fp32 ? launch_tile<true, 2, 4, 4, 2, 2>(p, stream) : launch_tile<false, 2, 4, 4, 2, 4>(p, stream);
 }
 
 }  // namespace llmoe
