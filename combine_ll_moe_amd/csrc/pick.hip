@@ -50,134 +50,434 @@ __device__ __forceinline__ float logit_at(const PickParams& P, int64_t at) {
 
 __device__ __forceinline__ double sigmoid(double l) { return 1.0 / (1.0 + exp(-l)); }
 
-// Weights of the picks of one row and their stores: lane k < topk holds pick
-// k, its expert (-1: none) and its logit; m and z are the softmax's.
-__device__ __forceinline__ void put_picks(const PickParams& P, int64_t row, int lane, int e, float logit, double m,
-                                          double z) {
-  const bool on = lane < P.topk && e >= 0;
-  const double l = logit;
-  double w = 0.0;
-  if (P.renormalize) {
-    const double top = wave_max(on ? l : none());
-    if (P.sigmoid) {
-      const double shift = fmin(top, 0.0);
-      w = l >= 0.0 ? 1.0 / (1.0 + exp(-l)) : exp(l - shift) / (1.0 + exp(l));
-    } else {
-      w = exp(l - top);
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v, uint32_t old = 0) {
+  return (uint32_t)__builtin_amdgcn_update_dpp((int)old, (int)v, CTRL, 0xF, 0xF, false);
+}
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float(dpp<CTRL>(__float_as_uint(v), __float_as_uint(v)));
+}
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return __longlong_as_double((long long)((uint64_t)dpp<CTRL>((uint32_t)(u >> 32)) << 32 | dpp<CTRL>((uint32_t)u)));
+}
+constexpr int kRor = 0x120, kShl = 0x100, kShr = 0x110;  // by n lanes of a row of 16
+
+__device__ __forceinline__ float row_max(float v) {
+  v = fmaxf(v, dpp<kRor + 8>(v));
+  v = fmaxf(v, dpp<kRor + 4>(v));
+  v = fmaxf(v, dpp<kRor + 2>(v));
+  return fmaxf(v, dpp<kRor + 1>(v));
+}
+__device__ __forceinline__ double row_sum(double v) {
+  v += dpp<kRor + 8>(v);
+  v += dpp<kRor + 4>(v);
+  v += dpp<kRor + 2>(v);
+  return v + dpp<kRor + 1>(v);
+}
+
+// How many of a row's 16 values are larger.
+template <int N = 1>
+__device__ __forceinline__ uint32_t rank(uint64_t v) {
+  const uint64_t other = (uint64_t)dpp<kRor + N>((uint32_t)(v >> 32)) << 32 | dpp<kRor + N>((uint32_t)v);
+  if constexpr (N < 15) return (other > v) + rank<N + 1>(v);
+  else return other > v;
+}
+
+// exp(x) for x <= 0, 1e-11 off at most: 2^n times the series of the rest,
+// |r| <= ln(2) / 2, whose tenth power over 10! is 7e-12.
+__device__ __forceinline__ double exp_series(double x) {
+  x = fmax(x, -750.0);
+  const double n = rint(x * 1.4426950408889634);
+  const double r = __builtin_fma(n, -0.69314718055994531, x);
+  double v = 1.0 / 362880;
+  v = __builtin_fma(v, r, 1.0 / 40320);
+  v = __builtin_fma(v, r, 1.0 / 5040);
+  v = __builtin_fma(v, r, 1.0 / 720);
+  v = __builtin_fma(v, r, 1.0 / 120);
+  v = __builtin_fma(v, r, 1.0 / 24);
+  v = __builtin_fma(v, r, 1.0 / 6);
+  v = __builtin_fma(v, r, 0.5);
+  v = __builtin_fma(v, r, 1.0);
+  v = __builtin_fma(v, r, 1.0);
+  return __builtin_ldexp(v, (int)n);
+}
+
+// Weights of a row's picks and their stores. Lane k < topk of a row of 16 holds
+// pick k, its expert (-1: none) and its logit; m and z are the softmax's. What
+// is rounded to fp32 is 1e-10 off at most.
+__device__ __forceinline__ void put(const PickParams& P, int64_t row, int k, int e, float logit, double m, double z,
+                                    bool store) {
+  const bool on = k < P.topk && e >= 0;
+  const double l = on ? (double)logit : 0.0;
+  double w;
+  if (P.sigmoid) {
+    const double x = exp_series(-fabs(l)), one = 1.0 / (1.0 + x);
+    w = l >= 0.0 ? one : x * one;
+    if (P.renormalize) {
+      // all below zero: without the common factor, that may be all there is
+      const float top = row_max(on ? logit : -__builtin_inff());
+      if (__ballot(top < 0.0f)) w = top < 0.0f ? exp_series(on ? l - (double)top : 0.0) * one : w;
     }
-    w = on ? w : 0.0;
-    const double sum = wave_sum(w);
-    w = on ? w / sum : 0.0;
-  } else if (on) {
-    w = P.sigmoid ? sigmoid(l) : exp(l - m) / z;
+  } else if (P.renormalize) {
+    const float top = row_max(on ? logit : -__builtin_inff());
+    w = exp_series(on ? l - (double)top : 0.0);
+  } else {
+    w = exp_series(on ? l - m : 0.0) / z;
   }
-  if (lane < P.topk) {
-    P.topk_idx[row * P.topk + lane] = e;
-    P.topk_weights[row * P.topk + lane] = (float)(w * (double)P.scale);
+  w = on ? w : 0.0;
+  if (P.renormalize) {
+    const double sum = row_sum(w);  // of all lanes, so outside the choice
+    w = on ? w / sum : 0.0;
+  }
+  if (store && k < P.topk) {
+    P.topk_idx[row * P.topk + k] = e;
+    P.topk_weights[row * P.topk + k] = (float)(w * (double)P.scale);
   }
 }
 
-// V: experts a lane holds, expert lane + 64 i in place i.
+// A row by a whole wavefront, everything in 64 bits. V: experts a lane holds,
+// expert lane + 64 i in place i; values: LDS for the experts' values, if there
+// are groups.
+template <int V>
+__device__ __forceinline__ void exact_row(const PickParams& P, int64_t row, int lane, double* values) {
+  const int E = P.num_experts, per = E / P.num_groups;
+      float l[V];
+  #pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = lane + 64 * i;
+        l[i] = e < E ? counted(logit_at(P, row * E + e)) : -__builtin_inff();
+      }
+      double m = 0.0, z = 1.0;
+      if (!P.sigmoid) {
+        m = none();
+  #pragma unroll
+        for (int i = 0; i < V; ++i) m = fmax(m, (double)l[i]);
+        m = wave_max(m);
+        z = 0.0;
+  #pragma unroll
+        for (int i = 0; i < V; ++i) z += l[i] > -__builtin_inff() ? exp((double)l[i] - m) : 0.0;
+        z = wave_sum(z);
+      }
+      auto score = [&](float x) { return P.sigmoid ? sigmoid(x) : exp((double)x - m) / z; };
+
+      double v[V];
+  #pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = lane + 64 * i;
+        const bool in = l[i] > -__builtin_inff();
+        if (P.bias) {
+          const float b = e < E ? counted(P.bias[e]) : -__builtin_inff();
+          v[i] = in && b > -__builtin_inff() ? score(l[i]) + (double)b : none();
+        } else {
+          v[i] = l[i];
+        }
+      }
+      if (P.num_groups > 1) {
+        const bool sums = !P.bias && P.group_best == 2;
+  #pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = lane + 64 * i;
+          if (e < E) values[e] = sums && l[i] > -__builtin_inff() ? score(l[i]) : v[i];
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        double best = none(), second = none();
+        if (lane < P.num_groups) {
+          for (int j = 0; j < per; ++j) {
+            const double x = values[lane * per + j];
+            second = fmax(second, fmin(best, x));
+            best = fmax(best, x);
+          }
+        }
+        const double mine = P.group_best == 2 ? best + second : best;
+        int before = 0;
+        for (int g = 0; g < P.num_groups; ++g) {
+          const double other = __shfl(mine, g, 64);
+          before += other > mine || (other == mine && g < lane);
+        }
+        const uint64_t kept = __ballot(lane < P.num_groups && before < P.topk_groups);
+  #pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const int e = lane + 64 * i;
+          if (e < E && !(kept >> (e / per) & 1)) v[i] = none();
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+
+      int pick = -1;
+      float pick_l = 0.0f;
+      for (int k = 0; k < P.topk; ++k) {
+        double best = none();
+        int e = INT32_MAX;
+        float bl = 0.0f;
+  #pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (v[i] > best) best = v[i], e = lane + 64 * i, bl = l[i];
+  #pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+          const double ov = __shfl_xor(best, d, 64);
+          const int oe = __shfl_xor(e, d, 64);
+          const float ol = __shfl_xor(bl, d, 64);
+          if (ov > best || (ov == best && oe < e)) best = ov, e = oe, bl = ol;
+        }
+        if (!(best > none())) break;
+  #pragma unroll
+        for (int i = 0; i < V; ++i)
+          if (lane + 64 * i == e) v[i] = none();
+        if (lane == k) pick = e, pick_l = bl;
+      }
+  put(P, row, lane, pick, pick_l, m, z, lane < 16);
+}
+
 template <int V>
 __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_kernel(const PickParams P) {
   extern __shared__ double values_raw[];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int E = P.num_experts, per = E / P.num_groups;
-  double* values = values_raw + wave * E;
   const int valid = P.num_valid ? *P.num_valid : P.num_tokens;
   for (int64_t row = (int64_t)blockIdx.x * kRowsAtOnce + wave; row < P.num_tokens;
        row += (int64_t)gridDim.x * kRowsAtOnce) {
-    if (row >= valid) {
-      put_picks(P, row, lane, -1, 0.0f, 0.0, 1.0);
-      continue;
-    }
-    float l[V];
+    if (row >= valid) put(P, row, lane, -1, 0.0f, 0.0, 1.0, lane < 16);
+    else exact_row<V>(P, row, lane, values_raw + wave * P.num_experts);
+  }
+}
+
+// Four rows a wavefront, 16 lanes each: the choice by fp32 values wherever
+// those decide it, and by exact_row where two that matter are within what
+// fp32 may be off by.
+
+// exact_row as a call of its own: rare, and its code and registers are not the
+// kernel's. It takes the parameters where the kernel's arguments stand (copies
+// of them for the call would be read from memory by the kernel, too).
+template <int V>
+__device__ __noinline__ void exact_row_apart(const PickParams* P, int64_t row, int lane, double* values) {
+  const PickParams p = *P;
+  exact_row<V>(p, row, lane, values);
+}
+__device__ __forceinline__ const PickParams* kernel_params() {
+  return (const PickParams*)__builtin_amdgcn_kernarg_segment_ptr();
+}
+
+// A value's bits in an order that unsigned numbers have.
+__device__ __forceinline__ uint32_t ordered(float v) {
+  const uint32_t u = __float_as_uint(v);
+  return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
+}
+__device__ __forceinline__ float unordered(uint32_t u) {
+  return __uint_as_float(u ^ ((uint32_t)((int32_t)~u >> 31) | 0x80000000u));
+}
+
+typedef uint32_t Words4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t Words2 __attribute__((ext_vector_type(2), aligned(4)));
+// N words from a 4-byte aligned address.
+template <int N>
+__device__ __forceinline__ void load_words(const void* from, uint32_t (&w)[N]) {
+  const uint32_t* at = static_cast<const uint32_t*>(from);
+  if constexpr (N == 2) {
+    const Words2 v = *reinterpret_cast<const Words2*>(at);
+    w[0] = v.x, w[1] = v.y;
+  } else {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      l[i] = e < E ? counted(logit_at(P, row * E + e)) : -__builtin_inff();
+    for (int i = 0; i < N; i += 4) {
+      const Words4 v = *reinterpret_cast<const Words4*>(at + i);
+      w[i] = v.x, w[i + 1] = v.y, w[i + 2] = v.z, w[i + 3] = v.w;
     }
+  }
+}
+
+// A row of 16 lanes holds a row's values, V a lane: expert lane * own + i if
+// the lanes have runs of experts (VEC: of V, read 16 bytes at a time), else
+// 16 i + lane.
+template <int V, bool VEC, bool BF16>
+__global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const PickParams P) {
+  extern __shared__ double values_raw[];
+  __shared__ uint64_t found[kRowsAtOnce][4][17];
+  __shared__ float2 found_lb[kRowsAtOnce][4][17];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, sub = lane >> 4;
+  const int E = P.num_experts;
+  const bool runs = VEC || P.num_groups > 1;
+  const int own = VEC ? V : (E + 15) / 16;
+  const float none32 = -__builtin_inff();
+  // what the values are: scores with a bias, or logits, whose order is exact
+  const bool scored = P.bias != nullptr;
+  const bool sums = P.num_groups > 1 && P.group_best == 2;
+  const bool group_scores = sums && !scored;
+  auto expert = [&](int i) { return runs ? l16 * own + i : 16 * i + l16; };
+  for (int64_t row0 = ((int64_t)blockIdx.x * kRowsAtOnce + wave) * 4; row0 < P.num_tokens;
+       row0 += (int64_t)gridDim.x * kRowsAtOnce * 4) {
+    // every load goes out before any is used; rows behind the last read it again
+    const int64_t row = row0 + sub, from = row < P.num_tokens ? row : P.num_tokens - 1;
+    const int valid = P.num_valid ? *P.num_valid : P.num_tokens;
+    float l[V], b[V];
+    if constexpr (VEC) {
+      uint32_t w[BF16 ? V / 2 : V], u[V];
+      load_words(static_cast<const uint8_t*>(P.logits) + (from * 16 + l16) * (V * (BF16 ? 2 : 4)), w);
+      if (scored) load_words(P.bias + l16 * V, u);
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        l[i] = __uint_as_float(!BF16 ? w[i] : i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
+        b[i] = __uint_as_float(u[i]);
+      }
+    } else {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const int e = expert(i);
+        const bool in = e < E && (!runs || i < own);
+        l[i] = in ? logit_at(P, from * E + e) : none32;
+        if (scored) b[i] = in ? P.bias[e] : none32;
+      }
+    }
+    const bool live = row < P.num_tokens && row < valid;
+    // one kind of zero: equal logits are equal numbers
+#pragma unroll
+    for (int i = 0; i < V; ++i) l[i] = counted(l[i]) + 0.0f;
+
+    // scores, where any are needed; the softmax's sum in 64 bits
     double m = 0.0, z = 1.0;
-    if (!P.sigmoid) {
-      m = none();
+    float s[V];
+    if (!P.sigmoid && (scored || group_scores || !P.renormalize)) {
+      float top = none32;
 #pragma unroll
-      for (int i = 0; i < V; ++i) m = fmax(m, (double)l[i]);
-      m = wave_max(m);
+      for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
+      m = row_max(top);
       z = 0.0;
 #pragma unroll
-      for (int i = 0; i < V; ++i) z += l[i] > -__builtin_inff() ? exp((double)l[i] - m) : 0.0;
-      z = wave_sum(z);
+      for (int i = 0; i < V; ++i) {
+        const double x = l[i] > none32 ? exp_series((double)l[i] - m) : 0.0;
+        s[i] = (float)x;
+        z += x;
+        if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few at a time, for the registers
+      }
+      z = row_sum(z);
+      const float inv = (float)(1.0 / z);
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] *= inv;
+    } else if (P.sigmoid && (scored || group_scores)) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
     }
-    auto score = [&](float x) { return P.sigmoid ? sigmoid(x) : exp((double)x - m) / z; };
+    float key[V];
+#pragma unroll
+    for (int i = 0; i < V; ++i) key[i] = l[i];
+    if (scored) {
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        b[i] = counted(b[i]) + 0.0f;
+        key[i] = l[i] > none32 ? s[i] + b[i] + 0.0f : none32;
+      }
+    }
 
-    double v[V];
+    // groups: 16 / num_groups lanes each
+    bool unsure = false;
+    if (P.num_groups > 1) {
+      float best = none32, second = none32;
+#pragma unroll
+      for (int i = 0; i < V; ++i) {
+        const float x = group_scores ? (l[i] > none32 ? s[i] : none32) : key[i];
+        second = fmaxf(second, fminf(best, x));
+        best = fmaxf(best, x);
+      }
+      const int lanes = 16 / P.num_groups;
+      auto join = [&](float ob, float os) {
+        second = fmaxf(fmaxf(second, os), fminf(best, ob));
+        best = fmaxf(best, ob);
+      };
+      // with the neighbour, the neighbouring pair, the neighbouring four
+      if (lanes >= 2) join(dpp<0xB1>(best), dpp<0xB1>(second));
+      if (lanes >= 4) join(dpp<0x4E>(best), dpp<0x4E>(second));
+      if (lanes >= 8) join(dpp<0x141>(best), dpp<0x141>(second));
+      const float mine = sums ? best + second : best;
+      // every lane of a better group stands before this one's
+      const bool kept = rank((uint64_t)ordered(mine) << 32 | (16 - l16 / lanes)) < (uint32_t)(P.topk_groups * lanes);
+      if (scored || group_scores) {
+        // the nearest values on both sides of the border, and how large
+        // anything in them is
+        const float in = -row_max(kept ? -mine : none32), out = row_max(kept ? none32 : mine);
+        const float size = row_max(best > none32 ? fabsf(best) + (sums && second > none32 ? fabsf(second) : 0.0f) : 0.0f);
+        unsure = out > none32 && !(in - out > 0x1p-19f + 0x1p-20f * size);
+      }
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : none32;
+    }
+
+    // A bound that at least topk values reach: the topk-th largest of the
+    // lanes' best two.
+    float first = none32, second = none32;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
-      const int e = lane + 64 * i;
-      const bool in = l[i] > -__builtin_inff();
-      if (P.bias) {
-        const float b = e < E ? counted(P.bias[e]) : -__builtin_inff();
-        v[i] = in && b > -__builtin_inff() ? score(l[i]) + (double)b : none();
-      } else {
-        v[i] = l[i];
-      }
+      second = fmaxf(second, fminf(first, key[i]));
+      first = fmaxf(first, key[i]);
     }
-    if (P.num_groups > 1) {
-      const bool sums = !P.bias && P.group_best == 2;
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E) values[e] = sums && l[i] > -__builtin_inff() ? score(l[i]) : v[i];
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-      double best = none(), second = none();
-      if (lane < P.num_groups) {
-        for (int j = 0; j < per; ++j) {
-          const double x = values[lane * per + j];
-          second = fmax(second, fmin(best, x));
-          best = fmax(best, x);
-        }
-      }
-      const double mine = P.group_best == 2 ? best + second : best;
-      int before = 0;
-      for (int g = 0; g < P.num_groups; ++g) {
-        const double other = __shfl(mine, g, 64);
-        before += other > mine || (other == mine && g < lane);
-      }
-      const uint64_t kept = __ballot(lane < P.num_groups && before < P.topk_groups);
-#pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const int e = lane + 64 * i;
-        if (e < E && !(kept >> (e / per) & 1)) v[i] = none();
-      }
-      __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-      __builtin_amdgcn_wave_barrier();
-    }
-
-    int pick = -1;
-    float pick_l = 0.0f;
+    float bound = none32;
     for (int k = 0; k < P.topk; ++k) {
-      double best = none();
-      int e = INT32_MAX;
-      float bl = 0.0f;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (v[i] > best) best = v[i], e = lane + 64 * i, bl = l[i];
-#pragma unroll
-      for (int d = 1; d < 64; d <<= 1) {
-        const double ov = __shfl_xor(best, d, 64);
-        const int oe = __shfl_xor(e, d, 64);
-        const float ol = __shfl_xor(bl, d, 64);
-        if (ov > best || (ov == best && oe < e)) best = ov, e = oe, bl = ol;
-      }
-      if (!(best > none())) break;
-#pragma unroll
-      for (int i = 0; i < V; ++i)
-        if (lane + 64 * i == e) v[i] = none();
-      if (lane == k) pick = e, pick_l = bl;
+      bound = row_max(first);
+      const bool taken = first == bound;
+      first = taken ? second : first;
+      second = taken ? none32 : second;
     }
-    put_picks(P, row, lane, pick, pick_l, m, z);
+    // Values nearer than this to each other may be in another order: a score's
+    // error is below 5 2^-24, its sum's with the bias half a step.
+    auto near = [&](float v) { return scored ? 0x1p-20f + 0x1p-21f * fabsf(v) : 0.0f; };
+    const float least = bound > none32 ? fmaxf(bound - near(bound), -FLT_MAX) : -FLT_MAX;
+
+    // the values that reach it, side by side in LDS
+    uint32_t count = 0;
+#pragma unroll
+    for (int i = 0; i < V; ++i) count += key[i] >= least;
+    uint32_t upto = count;
+    upto += dpp<kShr + 1>(upto);
+    upto += dpp<kShr + 2>(upto);
+    upto += dpp<kShr + 4>(upto);
+    upto += dpp<kShr + 8>(upto);
+    uint32_t all = upto;
+    all = max(all, dpp<kRor + 8>(all));
+    all = max(all, dpp<kRor + 4>(all));
+    all = max(all, dpp<kRor + 2>(all));
+    all = max(all, dpp<kRor + 1>(all));
+    uint32_t at = upto - count;
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (key[i] >= least && at < 16) {
+        found[wave][sub][at] = (uint64_t)ordered(key[i]) << 32 | (0xFFFFu - expert(i));
+        found_lb[wave][sub][at] = make_float2(l[i], scored ? b[i] : 0.0f);
+        ++at;
+      }
+    unsure |= all > 16;
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const bool in = (uint32_t)l16 < all;
+    const uint64_t mine = in ? found[wave][sub][l16] : 0;
+    const float2 mine_lb = found_lb[wave][sub][l16];
+    // a value's place is the number of larger ones (of equal ones with a
+    // smaller expert)
+    const uint32_t place = rank(mine);
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if (in) {
+      found[wave][sub][place] = mine;
+      found_lb[wave][sub][place] = mine_lb;
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    const uint64_t pick = in ? found[wave][sub][l16] : 0;
+    const float2 pick_lb = found_lb[wave][sub][l16];
+    const int e = in ? (int)(0xFFFFu - (uint32_t)pick) : -1;
+    if (scored) {
+      // neighbours too near to tell, unless logit and bias are the same
+      const float k0 = unordered((uint32_t)(pick >> 32));
+      const float k1 = dpp<kShl + 1>(k0), l1 = dpp<kShl + 1>(pick_lb.x), b1 = dpp<kShl + 1>(pick_lb.y);
+      unsure |= l16 < P.topk && (uint32_t)l16 + 1 < all && l16 < 15 &&
+                !(k0 - k1 > near(fmaxf(fabsf(k0), fabsf(k1)))) && !(pick_lb.x == l1 && pick_lb.y == b1);
+    }
+    // unsure rows again by the whole wavefront; the others' weights
+    const uint64_t again = __ballot(unsure && live);
+    put(P, row, l16, live ? e : -1, pick_lb.x, m, z, row < P.num_tokens && !(again >> (lane & 48) & 0xFFFF));
+    __builtin_amdgcn_wave_barrier();  // found is read before the next rows' values are written
+    for (int r = 0; r < 4; ++r)
+      if (again >> (16 * r) & 0xFFFF) exact_row_apart<(V + 3) / 4>(kernel_params(), row0 + r, lane, values_raw + wave * E);
   }
 }
 
@@ -190,15 +490,38 @@ hipError_t launch(const PickParams& p, hipStream_t stream) {
   return hipGetLastError();
 }
 
+template <int V, bool VEC>
+hipError_t launch_rows(const PickParams& p, hipStream_t stream) {
+  constexpr int ROWS = 4 * kRowsAtOnce;
+  const int64_t needed = ((int64_t)p.num_tokens + ROWS - 1) / ROWS;
+  const unsigned blocks = (unsigned)(needed < 1 << 16 ? needed : 1 << 16);
+  const uint32_t lds = p.num_groups > 1 ? kRowsAtOnce * p.num_experts * 8u : 0u;
+  if (p.bf16) pick_rows_kernel<V, VEC, true><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
+  else pick_rows_kernel<V, VEC, false><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
+  return hipGetLastError();
+}
+
 }  // namespace
 
+// Four rows a wavefront for up to 512 experts without groups, or with groups
+// that are whole lanes' runs of experts; else a row a wavefront.
 hipError_t launch_pick(const PickParams& p, hipStream_t stream) {
   if (p.num_tokens == 0) return hipSuccess;
-  if (p.num_experts <= 64) return launch<1>(p, stream);
-  if (p.num_experts <= 128) return launch<2>(p, stream);
-  if (p.num_experts <= 256) return launch<4>(p, stream);
-  if (p.num_experts <= 512) return launch<8>(p, stream);
-  if (p.num_experts <= 1024) return launch<16>(p, stream);
+  const int e = p.num_experts;
+  if (e <= 512 && (p.num_groups == 1 || (e % 16 == 0 && 16 % p.num_groups == 0))) {
+    if (e == 64) return launch_rows<4, true>(p, stream);
+    if (e == 128) return launch_rows<8, true>(p, stream);
+    if (e == 256) return launch_rows<16, true>(p, stream);
+    if (e == 512) return launch_rows<32, true>(p, stream);
+    if (e <= 64) return launch_rows<4, false>(p, stream);
+    if (e <= 128) return launch_rows<8, false>(p, stream);
+    return e <= 256 ? launch_rows<16, false>(p, stream) : launch_rows<32, false>(p, stream);
+  }
+  if (e <= 64) return launch<1>(p, stream);
+  if (e <= 128) return launch<2>(p, stream);
+  if (e <= 256) return launch<4>(p, stream);
+  if (e <= 512) return launch<8>(p, stream);
+  if (e <= 1024) return launch<16>(p, stream);
   return launch<64>(p, stream);
 }
 
