@@ -288,23 +288,25 @@ __device__ __forceinline__ void load_words(const void* from, uint32_t (&w)[N]) {
   }
 }
 
+// What the rows kernel goes by: values that are the logits, whose order is
+// exact, or scores with a bias.
+enum : int { kByLogits = 0, kBySigmoid = 1, kBySoftmax = 2 };
+
 // A row of 16 lanes holds a row's values, V a lane: expert lane * own + i if
 // the lanes have runs of experts (VEC: of V, read 16 bytes at a time), else
 // 16 i + lane.
-template <int V, bool VEC, bool BF16>
-__global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const PickParams P) {
+template <int V, bool VEC, int KIND>
+__global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickParams P) {
   extern __shared__ double values_raw[];
+  constexpr bool SCORED = KIND != kByLogits;
   __shared__ uint64_t found[kRowsAtOnce][4][17];
-  __shared__ float2 found_lb[kRowsAtOnce][4][17];
+  __shared__ float found_l[kRowsAtOnce][4][17];
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, l16 = lane & 15, sub = lane >> 4;
   const int E = P.num_experts;
   const bool runs = VEC || P.num_groups > 1;
   const int own = VEC ? V : (E + 15) / 16;
   const float none32 = -__builtin_inff();
-  // what the values are: scores with a bias, or logits, whose order is exact
-  const bool scored = P.bias != nullptr;
   const bool sums = P.num_groups > 1 && P.group_best == 2;
-  const bool group_scores = sums && !scored;
   auto expert = [&](int i) { return runs ? l16 * own + i : 16 * i + l16; };
   for (int64_t row0 = ((int64_t)blockIdx.x * kRowsAtOnce + wave) * 4; row0 < P.num_tokens;
        row0 += (int64_t)gridDim.x * kRowsAtOnce * 4) {
@@ -313,13 +315,21 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
     const int valid = P.num_valid ? *P.num_valid : P.num_tokens;
     float l[V], b[V];
     if constexpr (VEC) {
-      uint32_t w[BF16 ? V / 2 : V], u[V];
-      load_words(static_cast<const uint8_t*>(P.logits) + (from * 16 + l16) * (V * (BF16 ? 2 : 4)), w);
-      if (scored) load_words(P.bias + l16 * V, u);
+      uint32_t w[V], u[V];
+      if (P.bf16) {
+        uint32_t h[V / 2];
+        load_words(static_cast<const uint8_t*>(P.logits) + (from * 16 + l16) * (V * 2), h);
+        if (SCORED) load_words(P.bias + l16 * V, u);
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = i & 1 ? h[i / 2] & 0xFFFF0000u : h[i / 2] << 16;
+      } else {
+        load_words(static_cast<const uint8_t*>(P.logits) + (from * 16 + l16) * (V * 4), w);
+        if (SCORED) load_words(P.bias + l16 * V, u);
+      }
 #pragma unroll
       for (int i = 0; i < V; ++i) {
-        l[i] = __uint_as_float(!BF16 ? w[i] : i & 1 ? w[i / 2] & 0xFFFF0000u : w[i / 2] << 16);
-        b[i] = __uint_as_float(u[i]);
+        l[i] = __uint_as_float(w[i]);
+        if (SCORED) b[i] = __uint_as_float(u[i]);
       }
     } else {
 #pragma unroll
@@ -327,18 +337,18 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
         const int e = expert(i);
         const bool in = e < E && (!runs || i < own);
         l[i] = in ? logit_at(P, from * E + e) : none32;
-        if (scored) b[i] = in ? P.bias[e] : none32;
+        if (SCORED) b[i] = in ? P.bias[e] : none32;
       }
     }
     const bool live = row < P.num_tokens && row < valid;
-    // one kind of zero: equal logits are equal numbers
 #pragma unroll
-    for (int i = 0; i < V; ++i) l[i] = counted(l[i]) + 0.0f;
+    for (int i = 0; i < V; ++i) l[i] = counted(l[i]);
 
-    // scores, where any are needed; the softmax's sum in 64 bits
+    // The softmax's sum, in 64 bits, where anything needs it. The scores of
+    // groups without a bias need no sum: it is the same for all.
     double m = 0.0, z = 1.0;
-    float s[V];
-    if (!P.sigmoid && (scored || group_scores || !P.renormalize)) {
+    float key[V];
+    if (KIND == kBySoftmax || (KIND == kByLogits && !P.sigmoid && (sums || !P.renormalize))) {
       float top = none32;
 #pragma unroll
       for (int i = 0; i < V; ++i) top = fmaxf(top, l[i]);
@@ -347,70 +357,75 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const double x = l[i] > none32 ? exp_series((double)l[i] - m) : 0.0;
-        s[i] = (float)x;
+        if (SCORED) key[i] = (float)x;
         z += x;
         if (i % 4 == 3) __builtin_amdgcn_sched_barrier(0);  // a few at a time, for the registers
       }
       z = row_sum(z);
+    }
+    // the values
+    auto sigmoid32 = [](float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); };
+    if constexpr (SCORED) {
       const float inv = (float)(1.0 / z);
 #pragma unroll
-      for (int i = 0; i < V; ++i) s[i] *= inv;
-    } else if (P.sigmoid && (scored || group_scores)) {
-#pragma unroll
-      for (int i = 0; i < V; ++i) s[i] = __builtin_amdgcn_rcpf(1.0f + __expf(-l[i]));
-    }
-    float key[V];
-#pragma unroll
-    for (int i = 0; i < V; ++i) key[i] = l[i];
-    if (scored) {
-#pragma unroll
       for (int i = 0; i < V; ++i) {
-        b[i] = counted(b[i]) + 0.0f;
-        key[i] = l[i] > none32 ? s[i] + b[i] + 0.0f : none32;
+        const float s = KIND == kBySigmoid ? sigmoid32(l[i]) : key[i] * inv;
+        key[i] = l[i] > none32 ? s + counted(b[i]) : none32;
       }
+    } else {
+      // one kind of zero: equal logits are equal numbers
+#pragma unroll
+      for (int i = 0; i < V; ++i) key[i] = l[i] + 0.0f;
     }
+
+    // the lane's best two
+    float first = none32, second = none32;
+    auto enter = [&](float x) {
+      second = __builtin_amdgcn_fmed3f(first, second, x);
+      first = fmaxf(first, x);
+    };
+#pragma unroll
+    for (int i = 0; i < V; ++i) enter(key[i]);
 
     // groups: 16 / num_groups lanes each
     bool unsure = false;
     if (P.num_groups > 1) {
-      float best = none32, second = none32;
+      const float lane_first = first, lane_second = second;
+      if (!SCORED && sums) {
+        first = second = none32;
 #pragma unroll
-      for (int i = 0; i < V; ++i) {
-        const float x = group_scores ? (l[i] > none32 ? s[i] : none32) : key[i];
-        second = fmaxf(second, fminf(best, x));
-        best = fmaxf(best, x);
+        for (int i = 0; i < V; ++i) {
+          const float s = P.sigmoid ? sigmoid32(l[i]) : __expf(l[i] - (float)m);
+          enter(l[i] > none32 ? s : none32);
+        }
       }
       const int lanes = 16 / P.num_groups;
-      auto join = [&](float ob, float os) {
-        second = fmaxf(fmaxf(second, os), fminf(best, ob));
-        best = fmaxf(best, ob);
+      auto join = [&](float of, float os) {
+        second = fmaxf(fmaxf(second, os), fminf(first, of));
+        first = fmaxf(first, of);
       };
       // with the neighbour, the neighbouring pair, the neighbouring four
-      if (lanes >= 2) join(dpp<0xB1>(best), dpp<0xB1>(second));
-      if (lanes >= 4) join(dpp<0x4E>(best), dpp<0x4E>(second));
-      if (lanes >= 8) join(dpp<0x141>(best), dpp<0x141>(second));
-      const float mine = sums ? best + second : best;
+      if (lanes >= 2) join(dpp<0xB1>(first), dpp<0xB1>(second));
+      if (lanes >= 4) join(dpp<0x4E>(first), dpp<0x4E>(second));
+      if (lanes >= 8) join(dpp<0x141>(first), dpp<0x141>(second));
+      const float mine = sums ? first + second : first;
       // every lane of a better group stands before this one's
-      const bool kept = rank((uint64_t)ordered(mine) << 32 | (16 - l16 / lanes)) < (uint32_t)(P.topk_groups * lanes);
-      if (scored || group_scores) {
+      const bool kept = rank((uint64_t)ordered(mine) << 32 | (uint32_t)(16 - l16 / lanes)) < (uint32_t)(P.topk_groups * lanes);
+      if (SCORED || sums) {
         // the nearest values on both sides of the border, and how large
         // anything in them is
         const float in = -row_max(kept ? -mine : none32), out = row_max(kept ? none32 : mine);
-        const float size = row_max(best > none32 ? fabsf(best) + (sums && second > none32 ? fabsf(second) : 0.0f) : 0.0f);
+        const float size = row_max(first > none32 ? fabsf(first) + (sums && second > none32 ? fabsf(second) : 0.0f) : 0.0f);
         unsure = out > none32 && !(in - out > 0x1p-19f + 0x1p-20f * size);
       }
+      first = kept ? lane_first : none32;
+      second = kept ? lane_second : none32;
 #pragma unroll
       for (int i = 0; i < V; ++i) key[i] = kept ? key[i] : none32;
     }
 
     // A bound that at least topk values reach: the topk-th largest of the
     // lanes' best two.
-    float first = none32, second = none32;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-      second = fmaxf(second, fminf(first, key[i]));
-      first = fmaxf(first, key[i]);
-    }
     float bound = none32;
     for (int k = 0; k < P.topk; ++k) {
       bound = row_max(first);
@@ -420,7 +435,7 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
     }
     // Values nearer than this to each other may be in another order: a score's
     // error is below 5 2^-24, its sum's with the bias half a step.
-    auto near = [&](float v) { return scored ? 0x1p-20f + 0x1p-21f * fabsf(v) : 0.0f; };
+    auto near = [&](float v) { return SCORED ? 0x1p-20f + 0x1p-21f * fabsf(v) : 0.0f; };
     const float least = bound > none32 ? fmaxf(bound - near(bound), -FLT_MAX) : -FLT_MAX;
 
     // the values that reach it, side by side in LDS
@@ -442,7 +457,7 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
     for (int i = 0; i < V; ++i)
       if (key[i] >= least && at < 16) {
         found[wave][sub][at] = (uint64_t)ordered(key[i]) << 32 | (0xFFFFu - expert(i));
-        found_lb[wave][sub][at] = make_float2(l[i], scored ? b[i] : 0.0f);
+        if (SCORED) found_l[wave][sub][at] = l[i];
         ++at;
       }
     unsure |= all > 16;
@@ -450,7 +465,7 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
     __builtin_amdgcn_wave_barrier();
     const bool in = (uint32_t)l16 < all;
     const uint64_t mine = in ? found[wave][sub][l16] : 0;
-    const float2 mine_lb = found_lb[wave][sub][l16];
+    const float mine_l = SCORED && in ? found_l[wave][sub][l16] : 0.0f;
     // a value's place is the number of larger ones (of equal ones with a
     // smaller expert)
     const uint32_t place = rank(mine);
@@ -458,23 +473,25 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64, 1) pick_rows_kernel(const Pi
     __builtin_amdgcn_wave_barrier();
     if (in) {
       found[wave][sub][place] = mine;
-      found_lb[wave][sub][place] = mine_lb;
+      if (SCORED) found_l[wave][sub][place] = mine_l;
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const uint64_t pick = in ? found[wave][sub][l16] : 0;
-    const float2 pick_lb = found_lb[wave][sub][l16];
+    const float pick_key = unordered((uint32_t)(pick >> 32));
+    const float pick_l = !SCORED ? pick_key : in ? found_l[wave][sub][l16] : 0.0f;
     const int e = in ? (int)(0xFFFFu - (uint32_t)pick) : -1;
-    if (scored) {
+    if constexpr (SCORED) {
       // neighbours too near to tell, unless logit and bias are the same
-      const float k0 = unordered((uint32_t)(pick >> 32));
-      const float k1 = dpp<kShl + 1>(k0), l1 = dpp<kShl + 1>(pick_lb.x), b1 = dpp<kShl + 1>(pick_lb.y);
-      unsure |= l16 < P.topk && (uint32_t)l16 + 1 < all && l16 < 15 &&
-                !(k0 - k1 > near(fmaxf(fabsf(k0), fabsf(k1)))) && !(pick_lb.x == l1 && pick_lb.y == b1);
+      const float next = dpp<kShl + 1>(pick_key), next_l = dpp<kShl + 1>(pick_l);
+      const int next_e = (int)dpp<kShl + 1>((uint32_t)e);
+      const bool close = l16 < P.topk && (uint32_t)l16 + 1 < all && l16 < 15 &&
+                         !(pick_key - next > near(fmaxf(fabsf(pick_key), fabsf(next))));
+      if (close) unsure |= pick_l != next_l || counted(P.bias[e]) != counted(P.bias[next_e]);
     }
     // unsure rows again by the whole wavefront; the others' weights
     const uint64_t again = __ballot(unsure && live);
-    put(P, row, l16, live ? e : -1, pick_lb.x, m, z, row < P.num_tokens && !(again >> (lane & 48) & 0xFFFF));
+    put(P, row, l16, live ? e : -1, pick_l, m, z, row < P.num_tokens && !(again >> (lane & 48) & 0xFFFF));
     __builtin_amdgcn_wave_barrier();  // found is read before the next rows' values are written
     for (int r = 0; r < 4; ++r)
       if (again >> (16 * r) & 0xFFFF) exact_row_apart<(V + 3) / 4>(kernel_params(), row0 + r, lane, values_raw + wave * E);
@@ -496,8 +513,9 @@ hipError_t launch_rows(const PickParams& p, hipStream_t stream) {
   const int64_t needed = ((int64_t)p.num_tokens + ROWS - 1) / ROWS;
   const unsigned blocks = (unsigned)(needed < 1 << 16 ? needed : 1 << 16);
   const uint32_t lds = p.num_groups > 1 ? kRowsAtOnce * p.num_experts * 8u : 0u;
-  if (p.bf16) pick_rows_kernel<V, VEC, true><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
-  else pick_rows_kernel<V, VEC, false><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
+  if (!p.bias) pick_rows_kernel<V, VEC, kByLogits><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
+  else if (p.sigmoid) pick_rows_kernel<V, VEC, kBySigmoid><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
+  else pick_rows_kernel<V, VEC, kBySoftmax><<<blocks, kRowsAtOnce * 64, lds, stream>>>(p);
   return hipGetLastError();
 }
 
