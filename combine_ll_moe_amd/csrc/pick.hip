@@ -86,6 +86,22 @@ __device__ __forceinline__ uint32_t rank(uint64_t v) {
   else return other > v;
 }
 
+// The same of values and, where those are equal, smaller numbers.
+template <int N = 1>
+__device__ __forceinline__ uint32_t rank_by(double v, uint32_t number) {
+  const double ov = dpp<kRor + N>(v);
+  const uint32_t on = dpp<kRor + N>(number);  // lanes read each other: never behind a condition
+  const uint32_t before = ov > v || (ov == v && on < number);
+  if constexpr (N < 15) return before + rank_by<N + 1>(v, number);
+  else return before;
+}
+__device__ __forceinline__ double row_max(double v) {
+  v = fmax(v, dpp<kRor + 8>(v));
+  v = fmax(v, dpp<kRor + 4>(v));
+  v = fmax(v, dpp<kRor + 2>(v));
+  return fmax(v, dpp<kRor + 1>(v));
+}
+
 // exp(x) for x <= 0, 1e-11 off at most: 2^n times the series of the rest,
 // |r| <= ln(2) / 2, whose tenth power over 10! is 7e-12.
 __device__ __forceinline__ double exp_series(double x) {
@@ -103,6 +119,11 @@ __device__ __forceinline__ double exp_series(double x) {
   v = __builtin_fma(v, r, 1.0);
   v = __builtin_fma(v, r, 1.0);
   return __builtin_ldexp(v, (int)n);
+}
+
+__device__ __forceinline__ double sigmoid_series(double x) {
+  const double t = exp_series(-fabs(x)), one = 1.0 / (1.0 + t);
+  return x >= 0.0 ? one : t * one;
 }
 
 // Weights of a row's picks and their stores. Lane k < topk of a row of 16 holds
@@ -249,6 +270,12 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_kernel(const PickParams
 // those decide it, and by exact_row where two that matter are within what
 // fp32 may be off by.
 
+// Values' bits in an order that unsigned numbers have.
+__device__ __forceinline__ uint64_t ordered(double v) {
+  const uint64_t u = (uint64_t)__double_as_longlong(v);
+  return u ^ ((uint64_t)((int64_t)u >> 63) | 1ull << 63);
+}
+
 // exact_row as a call of its own: rare, and its code and registers are not the
 // kernel's. It takes the parameters where the kernel's arguments stand (copies
 // of them for the call would be read from memory by the kernel, too).
@@ -261,7 +288,6 @@ __device__ __forceinline__ const PickParams* kernel_params() {
   return (const PickParams*)__builtin_amdgcn_kernarg_segment_ptr();
 }
 
-// A value's bits in an order that unsigned numbers have.
 __device__ __forceinline__ uint32_t ordered(float v) {
   const uint32_t u = __float_as_uint(v);
   return u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
@@ -363,10 +389,17 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
       }
       z = row_sum(z);
     }
+    // A score to 1e-10 or better; those that a choice hangs on once fp32 cannot
+    // tell, and the weights.
+    auto score64 = [&](float x) {
+      if (KIND == kBySigmoid || (KIND == kByLogits && P.sigmoid)) return sigmoid_series(x);
+      return exp_series((double)x - m) / z;
+    };
     // the values
     auto sigmoid32 = [](float x) { return __builtin_amdgcn_rcpf(1.0f + __expf(-x)); };
+    const float inv = (float)(1.0 / z);
+    auto score32 = [&](float x) { return P.sigmoid ? sigmoid32(x) : __expf(x - (float)m) * inv; };
     if constexpr (SCORED) {
-      const float inv = (float)(1.0 / z);
 #pragma unroll
       for (int i = 0; i < V; ++i) {
         const float s = KIND == kBySigmoid ? sigmoid32(l[i]) : key[i] * inv;
@@ -395,8 +428,7 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
         first = second = none32;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-          const float s = P.sigmoid ? sigmoid32(l[i]) : __expf(l[i] - (float)m);
-          enter(l[i] > none32 ? s : none32);
+          enter(l[i] > none32 ? score32(l[i]) : none32);
         }
       }
       const int lanes = 16 / P.num_groups;
@@ -410,13 +442,48 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
       if (lanes >= 8) join(dpp<0x141>(first), dpp<0x141>(second));
       const float mine = sums ? first + second : first;
       // every lane of a better group stands before this one's
-      const bool kept = rank((uint64_t)ordered(mine) << 32 | (uint32_t)(16 - l16 / lanes)) < (uint32_t)(P.topk_groups * lanes);
+      const uint32_t stay = P.topk_groups * lanes;
+      bool kept = rank((uint64_t)ordered(mine) << 32 | (uint32_t)(16 - l16 / lanes)) < stay;
       if (SCORED || sums) {
         // the nearest values on both sides of the border, and how large
         // anything in them is
         const float in = -row_max(kept ? -mine : none32), out = row_max(kept ? none32 : mine);
         const float size = row_max(first > none32 ? fabsf(first) + (sums && second > none32 ? fabsf(second) : 0.0f) : 0.0f);
-        unsure = out > none32 && !(in - out > 0x1p-19f + 0x1p-20f * size);
+        const float off = 0x1p-19f + 0x1p-20f * size;
+        const bool tight = out > none32 && !(in - out > off);
+        if (__ballot(tight)) {
+          // The values of the groups again, to 1e-10, from the members that
+          // make them, if fp32 tells which those are: one value each within
+          // `off` of the first and of the second.
+          double top1 = none(), top2 = none();
+          uint32_t n1 = 0, n2 = 0;
+#pragma unroll
+          for (int i = 0; i < V; ++i) {
+            const float x = !SCORED && sums ? (l[i] > none32 ? score32(l[i]) : none32) : key[i];
+            const bool is1 = x > none32 && x >= first - off, is2 = x > none32 && !is1 && x >= second - off;
+            if (is1 || (is2 && sums)) {
+              const double v = score64(l[i]) + (SCORED ? (double)counted(b[i]) : 0.0);
+              if (is1) top1 = v, ++n1;
+              else top2 = v, ++n2;
+            }
+          }
+          auto join64 = [&](double o1, double o2, uint32_t c1, uint32_t c2) {
+            top1 = fmax(top1, o1), top2 = fmax(top2, o2), n1 += c1, n2 += c2;
+          };
+          if (lanes >= 2) join64(dpp<0xB1>(top1), dpp<0xB1>(top2), dpp<0xB1>(n1), dpp<0xB1>(n2));
+          if (lanes >= 4) join64(dpp<0x4E>(top1), dpp<0x4E>(top2), dpp<0x4E>(n1), dpp<0x4E>(n2));
+          if (lanes >= 8) join64(dpp<0x141>(top1), dpp<0x141>(top2), dpp<0x141>(n1), dpp<0x141>(n2));
+          const double exact = sums ? top1 + top2 : top1;
+          const bool told = mine == none32 || (n1 == 1 && (!sums || n2 == 1));
+          const bool at_border = mine > none32 && !(fabsf(mine - in) > off && fabsf(mine - out) > off);
+          const bool kept64 = rank((uint64_t)ordered(exact)) < stay;
+          const double in64 = -row_max(kept64 ? -exact : none()), out64 = row_max(kept64 ? none() : exact);
+          const double off64 = 0x1p-30 + 0x1p-48 * (double)size;
+          // (the border of 64 bits must not be a tie either)
+          const bool left = (at_border && !told) || !(in64 - out64 > off64);
+          unsure = tight && row_max(left ? 1.0f : 0.0f) > 0.0f;
+          kept = tight ? kept64 : kept;
+        }
       }
       first = kept ? lane_first : none32;
       second = kept ? lane_second : none32;
@@ -479,15 +546,37 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
     __builtin_amdgcn_wave_barrier();
     const uint64_t pick = in ? found[wave][sub][l16] : 0;
     const float pick_key = unordered((uint32_t)(pick >> 32));
-    const float pick_l = !SCORED ? pick_key : in ? found_l[wave][sub][l16] : 0.0f;
-    const int e = in ? (int)(0xFFFFu - (uint32_t)pick) : -1;
+    float pick_l = !SCORED ? pick_key : in ? found_l[wave][sub][l16] : 0.0f;
+    int e = in ? (int)(0xFFFFu - (uint32_t)pick) : -1;
     if constexpr (SCORED) {
-      // neighbours too near to tell, unless logit and bias are the same
-      const float next = dpp<kShl + 1>(pick_key), next_l = dpp<kShl + 1>(pick_l);
-      const int next_e = (int)dpp<kShl + 1>((uint32_t)e);
-      const bool close = l16 < P.topk && (uint32_t)l16 + 1 < all && l16 < 15 &&
-                         !(pick_key - next > near(fmaxf(fabsf(pick_key), fabsf(next))));
-      if (close) unsure |= pick_l != next_l || counted(P.bias[e]) != counted(P.bias[next_e]);
+      // neighbours too near to tell
+      const float next = dpp<kShl + 1>(pick_key);
+      const bool last = l16 >= P.topk || (uint32_t)l16 + 1 >= all || l16 == 15;
+      const bool close = !last && !(pick_key - next > near(fmaxf(fabsf(pick_key), fabsf(next))));
+      if (__ballot(close)) {
+        // the row's values again, to 1e-10, and their places by those
+        const float pick_b = in ? counted(P.bias[e]) : 0.0f;
+        const double v = in ? score64(pick_l) + (double)pick_b : none();
+        const uint32_t again = rank_by(v, (uint32_t)e);
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (in) {
+          found[wave][sub][again] = (uint64_t)__float_as_uint(pick_b) << 32 | (uint32_t)e;
+          found_l[wave][sub][again] = pick_l;
+        }
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+        if (in) {
+          e = (int)(uint32_t)found[wave][sub][l16];
+          pick_l = found_l[wave][sub][l16];
+        }
+        const float in_b = in ? __uint_as_float((uint32_t)(found[wave][sub][l16] >> 32)) : 0.0f;
+        const double in_v = in ? score64(pick_l) + (double)in_b : none();
+        const double next_v = dpp<kShl + 1>(in_v);
+        const float next_l = dpp<kShl + 1>(pick_l), next_b = dpp<kShl + 1>(in_b);
+        const bool same = pick_l == next_l && in_b == next_b;
+        unsure |= !last && !same && !(in_v - next_v > 0x1p-30 + 0x1p-48 * fabs(in_v));
+      }
     }
     // unsure rows again by the whole wavefront; the others' weights
     const uint64_t again = __ballot(unsure && live);

@@ -197,3 +197,59 @@ def test_captured_calls_follow_the_valid_count():
         graph.replay()
         torch.cuda.synchronize()
         R.check(idx.cpu(), w.cpu(), x.cpu().numpy(), b.cpu().numpy(), n, 8, True, 8, 4, 2, True, 2.5)
+
+
+def _sigmoid_near(target, rng):
+    """fp32 logits whose sigmoids are within fp32's rounding of `target`."""
+    x = np.float32(np.log(target / (1 - target)))
+    return (x.view(np.int32) + np.int32(rng.integers(-3, 4))).view(np.float32)
+
+
+@pytest.mark.parametrize("e,groups,topk_groups,best", [(256, 1, 1, 1), (256, 8, 4, 2), (128, 4, 2, 1), (100, 1, 1, 1),
+                                                       (64, 16, 5, 2), (512, 2, 1, 2), (96, 8, 3, 2)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_single_pairs_within_32_bit_rounding(e, groups, topk_groups, best, sigmoid):
+    """Each row has a pair of experts with different biases whose values differ
+    by some 1e-8, among the largest: the choice of fp32 would be a toss."""
+    rng = np.random.default_rng(e + groups)
+    rows = rng.standard_normal((96, e)).astype(np.float32)
+    bias = (rng.standard_normal(e) * 0.05).astype(np.float32)
+    for t, row in enumerate(rows):
+        a, c = rng.choice(e, 2, replace=False)
+        if sigmoid:
+            value = 0.9 + 0.01 * rng.random()
+            row[a], row[c] = (_sigmoid_near(value - bias[x], rng) for x in (a, c))
+        else:
+            # their scores and biases sum up alike: p_c = p_a + b_a - b_c, the
+            # rest of the row giving the sum
+            rest = np.exp(np.delete(row.astype(np.float64), (a, c))).sum()
+            pa = 0.3
+            pc = pa + float(bias[a]) - float(bias[c])
+            z = rest / (1 - pa - pc)
+            row[a], row[c] = np.float32(np.log(pa * z)), np.float32(np.log(pc * z))
+    x, b = torch.from_numpy(rows).to(DEV), torch.from_numpy(bias).to(DEV)
+    verify(x, 4, sigmoid, b, groups, topk_groups, best, True, 1.0)
+    verify(x, 1, sigmoid, b, groups, topk_groups, best, False, 2.0)
+
+
+@pytest.mark.parametrize("e,groups,topk_groups", [(256, 8, 4), (128, 4, 1), (64, 16, 7), (512, 2, 1), (96, 8, 3), (60, 6, 2)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("with_bias", [True, False])
+def test_groups_within_32_bit_rounding(e, groups, topk_groups, best, with_bias):
+    """The last group that stays and the first that does not differ by some
+    1e-8; sometimes more than one of a group's members are near its best."""
+    rng = np.random.default_rng(e + groups + best)
+    rows = (rng.standard_normal((80, e)) - 1).astype(np.float32)
+    bias = (rng.standard_normal(e) * 0.05).astype(np.float32) if with_bias else np.zeros(e, np.float32)
+    per = e // groups
+    for t, row in enumerate(rows):
+        order = rng.permutation(groups)
+        for place, g in enumerate(order):
+            at = g * per + rng.choice(per, min(best + (t % 3 == 0), per), replace=False)
+            # values fall from group to group, but for the border's two
+            step = min(place, topk_groups - 1) if place <= topk_groups else place
+            for x in at:
+                row[x] = _sigmoid_near(0.75 - 0.02 * step - bias[x], rng)
+    x = torch.from_numpy(rows).to(DEV)
+    b = torch.from_numpy(bias).to(DEV) if with_bias else None
+    verify(x, min(4, topk_groups * per), True, b, groups, topk_groups, best, True, 1.0)
