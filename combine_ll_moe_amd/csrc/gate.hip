@@ -7,9 +7,16 @@
 // matrix cores have no fp32 product of this rate. (A weight that is not finite
 // has NaN for its rest.)
 //
-// Design: a workgroup has 16 tokens x 16 experts; its eight wavefronts split
-// the columns and add up through LDS. Rows come by whole lines into
-// registers, some steps ahead, and through LDS into the products' order.
+// Design, by how much work there is (launch_gate): a wavefront with one
+// expert's row (gate_row_kernel); 16 tokens by a few experts, whose columns are
+// split among the wavefronts (gate_few_kernel); tiles that come straight into
+// LDS, steps ahead of the products (gate_tile_kernel).
+//
+// Bound: one token 3.5 us with bf16 weights (3.7 MB) and a decode batch 7 are
+// latency: a launch, loads, and the sums' meeting. 16384 tokens (hidden 7168,
+// 256 experts, bf16) take 79 us, 760 TFLOP/s; their operands pass from the
+// caches to LDS at 12 TB/s, and each SIMD's one or two wavefronts wait for each
+// other at every step.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -19,9 +26,10 @@
 namespace llmoe {
 namespace {
 
-constexpr int kWaves = 8;
 constexpr int kColumns = 64;  // of a step
-constexpr int64_t kFewLogits = 1 << 18, kManyTiles = 192;
+constexpr int kRowTokens = 4;
+constexpr int64_t kFewLogits = 3 << 16, kFewLogitsFp32 = 1 << 18;
+constexpr int64_t kCus = 256;
 
 __device__ __forceinline__ uint32_t opaque_zero() {
   uint32_t zero = 0;
@@ -56,14 +64,70 @@ __device__ __forceinline__ Parts cut(v4u a, v4u b) {
   return o;
 }
 
-template <bool FP32>
-__global__ void __launch_bounds__(kWaves * 64) gate_few_kernel(const GateParams P) {
-  constexpr int ITEM = FP32 ? 4 : 2, WROW = kColumns * ITEM, WL = FP32 ? 4 : 2, D = 4;
-  constexpr int XPART = 16 * 128, WPART = 16 * WROW;
-  __shared__ __align__(16) uint8_t pool[kWaves * (XPART + WPART)];
+// A few tokens: a wavefront has one expert, every lane 8 columns at a time.
+template <bool FP32, int T>
+__global__ void __launch_bounds__(64) gate_row_kernel(const GateParams P) {
+  constexpr int D = 8;  // loads of W under way
+  const int lane = threadIdx.x, e = blockIdx.x;
+  const uint32_t ldx = (uint32_t)P.hidden * 2, ldw = (uint32_t)P.hidden * (FP32 ? 4 : 2);
+  const Rsrc rw = rsrc_of(P.w + (uint64_t)e * ldw, ldw);
+  const Rsrc rx = rsrc_of(P.x, (uint32_t)P.num_tokens * ldx);
+  const int steps = (P.hidden + 511) / 512;
+  v4u wb[D][FP32 ? 2 : 1], xb[D][T];
+  auto load = [&](int s, int step) {
+    const uint32_t c = (uint32_t)step * 512 + lane * 8;
+    const bool in = c < (uint32_t)P.hidden;
+#pragma unroll
+    for (int i = 0; i < (FP32 ? 2 : 1); ++i)
+      wb[s][i] = __builtin_amdgcn_raw_buffer_load_b128(rw, (int)(in ? c * (FP32 ? 4 : 2) + 16 * i : kOutside), 0, 0);
+#pragma unroll
+    for (int t = 0; t < T; ++t)
+      xb[s][t] = __builtin_amdgcn_raw_buffer_load_b128(rx, (int)(in ? t * ldx + c * 2 : kOutside), 0, 0);
+  };
+  float sum[T] = {};
+#pragma unroll
+  for (int s = 0; s < D; ++s) load(s, s);
+  for (int k = 0; k < steps; k += D) {
+#pragma unroll
+    for (int s = 0; s < D; ++s) {
+      float w[8];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if constexpr (FP32) {
+          w[i] = __uint_as_float(wb[s][0][i]);
+          w[4 + i] = __uint_as_float(wb[s][1][i]);
+        } else {
+          w[2 * i] = __uint_as_float(wb[s][0][i] << 16);
+          w[2 * i + 1] = __uint_as_float(wb[s][0][i] & 0xFFFF0000u);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < T; ++t)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          sum[t] = __builtin_fmaf(__uint_as_float(xb[s][t][i] << 16), w[2 * i], sum[t]);
+          sum[t] = __builtin_fmaf(__uint_as_float(xb[s][t][i] & 0xFFFF0000u), w[2 * i + 1], sum[t]);
+        }
+      load(s, k + s + D);
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < T; ++t) {
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) sum[t] += __shfl_xor(sum[t], d, 64);
+    if (lane == 0 && t < P.num_tokens) P.logits[(int64_t)t * P.num_experts + e] = sum[t];
+  }
+}
+
+// 16 tokens x EW experts (16, or 8 where that gives the GPU more to do at once).
+template <bool FP32, int EW, int WAVES, int D>
+__global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P) {
+  constexpr int ITEM = FP32 ? 4 : 2, WROW = kColumns * ITEM, WL = (EW * WROW + 1023) / 1024;
+  constexpr int XPART = 16 * 128, WPART = EW * WROW;
+  __shared__ __align__(16) uint8_t pool[WAVES * (XPART + WPART)];
   const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int across = (P.num_experts + 15) / 16, down = (P.num_tokens + 15) / 16;
+  const int across = (P.num_experts + EW - 1) / EW, down = (P.num_tokens + 15) / 16;
   uint8_t* xl = pool + wave * (XPART + WPART);
   uint8_t* wl = xl + XPART;
   const uint32_t apart = opaque_zero();  // lanes read each other's rows
@@ -71,13 +135,13 @@ __global__ void __launch_bounds__(kWaves * 64) gate_few_kernel(const GateParams 
   const uint8_t* wr = wl + apart;
   const uint32_t ldx = (uint32_t)P.hidden * 2, ldw = (uint32_t)P.hidden * ITEM;
   const int steps = (P.hidden + kColumns - 1) / kColumns;
-  const int s0 = steps * wave / kWaves, s1 = steps * (wave + 1) / kWaves;
+  const int s0 = steps * wave / WAVES, s1 = steps * (wave + 1) / WAVES;
   const int64_t tiles = (int64_t)across * down;
   for (int64_t t = blockIdx.x; t < tiles; t += gridDim.x) {
-    const int e0 = (int)(t % across) * 16;
+    const int e0 = (int)(t % across) * EW;
     const int64_t row0 = t / across * 16;
     const int rows = P.num_tokens - row0 < 16 ? (int)(P.num_tokens - row0) : 16;
-    const int experts = P.num_experts - e0 < 16 ? P.num_experts - e0 : 16;
+    const int experts = P.num_experts - e0 < EW ? P.num_experts - e0 : EW;
     const Rsrc rx = rsrc_of(P.x + (uint64_t)row0 * ldx, (uint32_t)rows * ldx);
     const Rsrc rw = rsrc_of(P.w + (uint64_t)e0 * ldw, (uint32_t)experts * ldw);
     v4u xb[D][2], wb[D][WL];
@@ -93,7 +157,9 @@ __global__ void __launch_bounds__(kWaves * 64) gate_few_kernel(const GateParams 
         constexpr int CH = WROW / 16;
         const uint32_t at = (uint32_t)step * WROW + (lane % CH) * 16;
         wb[s][i] = __builtin_amdgcn_raw_buffer_load_b128(
-            rw, (int)(step < s1 && at < ldw ? (lane / CH + 64 / CH * i) * ldw + at : kOutside), 0, 0);
+            rw, (int)(step < s1 && at < ldw && lane / CH + 64 / CH * i < EW ? (lane / CH + 64 / CH * i) * ldw + at
+                                                                             : kOutside),
+            0, 0);
       }
     };
     auto store = [&](int s) {
@@ -106,24 +172,25 @@ __global__ void __launch_bounds__(kWaves * 64) gate_few_kernel(const GateParams 
       for (int i = 0; i < WL; ++i) {
         constexpr int CH = WROW / 16;
         const int r = lane / CH + 64 / CH * i, c = lane % CH;
-        *reinterpret_cast<v4u*>(wl + r * WROW + ((c ^ r) & (CH - 1)) * 16) = wb[s][i];
+        if (64 / CH <= EW || r < EW) *reinterpret_cast<v4u*>(wl + r * WROW + ((c ^ r) & (CH - 1)) * 16) = wb[s][i];
       }
     };
-    auto chunk = [&](const uint8_t* from, int row_bytes, int c) {
-      return *reinterpret_cast<const v4u*>(from + lo * row_bytes + ((c ^ lo) & (row_bytes / 16 - 1)) * 16);
+    auto chunk = [&](const uint8_t* from, int r, int row_bytes, int c) {
+      return *reinterpret_cast<const v4u*>(from + r * row_bytes + ((c ^ r) & (row_bytes / 16 - 1)) * 16);
     };
+    const int wrow = lo & (EW - 1);
     f32x4 acc = {0, 0, 0, 0};
     auto multiply = [&] {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const bf16x8 a = __builtin_bit_cast(bf16x8, chunk(xr, 128, 4 * j + hi));
+        const bf16x8 a = __builtin_bit_cast(bf16x8, chunk(xr, lo, 128, 4 * j + hi));
         if constexpr (FP32) {
-          const Parts w = cut(chunk(wr, WROW, 8 * j + 2 * hi), chunk(wr, WROW, 8 * j + 2 * hi + 1));
+          const Parts w = cut(chunk(wr, wrow, WROW, 8 * j + 2 * hi), chunk(wr, wrow, WROW, 8 * j + 2 * hi + 1));
 #pragma unroll
           for (int p = 0; p < 3; ++p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.part[p], a, acc, 0, 0, 0);
         } else {
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, chunk(wr, WROW, 4 * j + hi)), a, acc,
-                                                       0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, chunk(wr, wrow, WROW, 4 * j + hi)), a,
+                                                        acc, 0, 0, 0);
         }
       }
     };
@@ -147,7 +214,7 @@ __global__ void __launch_bounds__(kWaves * 64) gate_few_kernel(const GateParams 
     if (threadIdx.x < 256) {
       float v = 0.0f;
 #pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += sums[w * 256 + threadIdx.x];
+      for (int w = 0; w < WAVES; ++w) v += sums[w * 256 + threadIdx.x];
       const int r = threadIdx.x / 16, e = threadIdx.x % 16;
       if (r < rows && e < experts) P.logits[(row0 + r) * P.num_experts + e0 + e] = v;
     }
@@ -292,30 +359,59 @@ hipError_t launch_tile(const GateParams& p, hipStream_t stream) {
   return hipSuccess;
 }
 
-template <bool FP32>
+template <bool FP32, int EW, int WAVES, int D>
 hipError_t launch_few(const GateParams& p, hipStream_t stream) {
-  const int64_t tiles = (((int64_t)p.num_tokens + 15) / 16) * ((p.num_experts + 15) / 16);
+  const int64_t tiles = (((int64_t)p.num_tokens + 15) / 16) * ((p.num_experts + EW - 1) / EW);
   const unsigned blocks = (unsigned)(tiles < 1 << 16 ? tiles : 1 << 16);
-  gate_few_kernel<FP32><<<blocks, kWaves * 64, 0, stream>>>(p);
+  gate_few_kernel<FP32, EW, WAVES, D><<<blocks, WAVES * 64, 0, stream>>>(p);
+  return hipGetLastError();
+}
+
+template <bool FP32>
+hipError_t launch_row(const GateParams& p, hipStream_t stream) {
+  if (p.num_tokens == 1) gate_row_kernel<FP32, 1><<<p.num_experts, 64, 0, stream>>>(p);
+  else if (p.num_tokens == 2) gate_row_kernel<FP32, 2><<<p.num_experts, 64, 0, stream>>>(p);
+  else gate_row_kernel<FP32, 4><<<p.num_experts, 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
 }  // namespace
 
-// Which kernel: the first up to kFewLogits logits (bf16, hidden 7168 and 256
-// experts: 512 tokens 15.5 us against 23.5 in tiles of 64 x 64, 1024 tokens 30
-// against 29; fp32 1024 tokens 55 against 82, 2048 tokens 108 against 82). Then
-// tiles of 64 x 64, and of 128 x 128 where those are kManyTiles or more (4096
-// tokens: 36 us against 68; 16384 tokens: 118 against 80, fp32 257 against 196).
+// Which kernel, by the sizes (us at hidden 7168 and 256 experts, weights bf16 |
+// fp32). Up to kRowTokens tokens: a wavefront an expert (1 token 3.5 | 4.2, where
+// 16 x 8 take 6.0 | 9.6; 4 tokens 6.1 | 6.5 against 6.0 | 9.8). Then 16 tokens
+// by as few experts as fill the GPU once (64 tokens: 16 x 4 6.8 | 9.6, 16 x 8 6.8 |
+// 10.6, 16 x 16 8.3 | 12.7), up to as many logits as tiles do faster (768
+// tokens 19.7 against 21.3, 1024 tokens 31 against 24 | 46 against 48). Then the
+// smallest tiles that are not too many: 64 x 32 (2048 tokens 29 | 49, in 64 x 64
+// 34 | 79; 4096 tokens 49 | 75), bf16 64 x 64 (4096 tokens 36, 8192 63; in
+// 128 x 128 67, 69), fp32 128 x 32 (8192 tokens 110, in 64 x 32 141), 128 x 64
+// (16384 tokens 188, in 128 x 32 207), bf16 128 x 128 (16384 tokens 79, in 64 x
+// 64 118).
 hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   if (p.num_tokens == 0) return hipSuccess;
+  auto tiles = [&](int64_t tokens, int64_t experts) {
+    return (p.num_tokens + tokens - 1) / tokens * ((p.num_experts + experts - 1) / experts);
+  };
+  if (p.num_tokens <= kRowTokens) return p.w_fp32 ? launch_row<true>(p, stream) : launch_row<false>(p, stream);
   const int64_t logits = (int64_t)p.num_tokens * p.num_experts;
-  if (logits <= (p.w_fp32 ? kFewLogits * 3 / 2 : kFewLogits))
-    return p.w_fp32 ? launch_few<true>(p, stream) : launch_few<false>(p, stream);
-  const int64_t tiles = (((int64_t)p.num_tokens + 127) / 128) * ((p.num_experts + 127) / 128);
-  if (tiles < kManyTiles)
-    return p.w_fp32 ? launch_tile<true, 2, 2, 2, 2, 3>(p, stream) : launch_tile<false, 2, 2, 2, 2, 4>(p, stream);
-  return p.w_fp32 ? launch_tile<true, 2, 4, 4, 2, 2>(p, stream) : launch_tile<false, 2, 4, 4, 2, 4>(p, stream);
+  if (p.w_fp32) {
+    if (logits <= kFewLogitsFp32) {
+      if (tiles(16, 4) <= kCus) return launch_few<true, 4, 16, 2>(p, stream);
+      if (tiles(16, 8) <= kCus) return launch_few<true, 8, 16, 2>(p, stream);
+      return tiles(16, 16) <= kCus ? launch_few<true, 16, 16, 2>(p, stream) : launch_few<true, 16, 8, 2>(p, stream);
+    }
+    if (tiles(64, 32) <= 2 * kCus) return launch_tile<true, 2, 2, 2, 1, 4>(p, stream);
+    return tiles(128, 64) < 2 * kCus ? launch_tile<true, 2, 2, 4, 1, 2>(p, stream)
+                                     : launch_tile<true, 2, 2, 4, 2, 2>(p, stream);
+  }
+  if (logits <= kFewLogits) {
+    if (tiles(16, 8) <= kCus) return launch_few<false, 8, 16, 2>(p, stream);
+    return tiles(16, 16) <= kCus ? launch_few<false, 16, 16, 2>(p, stream) : launch_few<false, 16, 8, 2>(p, stream);
+  }
+  if (tiles(64, 32) <= kCus) return launch_tile<false, 2, 2, 2, 1, 4>(p, stream);
+  return tiles(128, 128) < kCus * 3 / 4 ? launch_tile<false, 2, 2, 2, 2, 4>(p, stream)
+                                        : launch_tile<false, 2, 4, 4, 2, 4>(p, stream);
 }
 
 }  // namespace llmoe
