@@ -27,9 +27,12 @@ namespace {
 enum : int { kPartial = 0, kPlain = 1, kGated = 2, kGatedFp8 = 3 };
 static_assert(kStep == kFp8Block);  // a k step is one scale's columns
 constexpr int64_t kWorkspace = LL_MOE_DENSE_WORKSPACE;
-// Rows up to which a tile has 16, 64 and 128 of them, and steps of k that a
-// split has to save, to be worth its second kernel.
-constexpr int kFewTokens = 32, kSomeTokens = 256, kSomeGatedTokens = 128, kManyTokens = 4096;
+// Workgroups up to which there are enough of 16 x 16; rows up to which a tile
+// has 16, 64 and 128 of them; steps of k that a split has to save, to be worth
+// its second kernel (1 row, n 7168, k 2048: 7.2 us, in two runs 8.2; 17 rows, n
+// 1040, k 4096: 10.4 us, in four runs 8.0).
+constexpr int kFew = 512, kFewToFp8 = 256;
+constexpr int kTokens16 = 32, kTokens16Gated = 16, kTokens64 = 256, kTokens64Gated = 128, kTokens128 = 4096;
 constexpr int kWorthSplit = 12;
 
 // WM x WN wavefronts, each FM x FN fragments of 16 x 16; STAGES buffers of a
@@ -242,6 +245,107 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams
   }
 }
 
+// A few rows: 16 rows of A by 16 of W, whose columns the wavefronts split and
+// whose sums meet in LDS, so that one launch does it. Gated, the 16 are 8 gate
+// rows and the 8 up rows of the same columns; their values go out in bf16, or
+// (kValues) in fp32 to the workspace, for dense_finish_kernel to quantize.
+// Rows come by whole lines into registers, D steps ahead, and through LDS
+// into the products' order.
+enum : int { kValues = 4 };
+template <int WAVES, int D, int MODE>
+__global__ void __launch_bounds__(WAVES * 64) dense_few_kernel(const DenseParams P) {
+  constexpr bool GATED = MODE != kPlain;
+  constexpr int COLS = GATED ? 8 : 16, PART = 16 * kStep;
+  __shared__ __align__(16) uint8_t pool[WAVES * 2 * PART];
+  const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const uint32_t ld = (uint32_t)P.k;
+  const int kb = P.k / 128;
+  const int s0 = kb * wave / WAVES, s1 = kb * (wave + 1) / WAVES;
+  const uint32_t across = (uint32_t)(P.n / COLS);
+  const int64_t row0 = (int64_t)(blockIdx.x / across) * 16;
+  const int col0 = (int)(blockIdx.x % across) * COLS;
+  const int rows = P.m - row0 < 16 ? (int)(P.m - row0) : 16;
+  const int second = GATED ? P.n + col0 : col0 + 8;  // rows 8-15 of W
+  const Rsrc ra = rsrc_of(P.a + (uint64_t)row0 * ld, (uint32_t)rows * ld);
+  const Rsrc rw0 = rsrc_of(P.w + (uint64_t)col0 * ld, 8 * ld), rw1 = rsrc_of(P.w + (uint64_t)second * ld, 8 * ld);
+  const Rsrc ras = rsrc_of(P.a_scales + (uint64_t)row0 * kb, (uint32_t)rows * kb * 4u);
+  const Rsrc rws = rsrc_of(P.w_scales, (uint32_t)((GATED ? 2 * P.n : P.n) + 127) / 128 * kb * 4u);
+  const uint32_t my_block = 4u * (uint32_t)((hi < 2 ? col0 : second) / 128 * kb);
+  uint8_t* al = pool + wave * 2 * PART;
+  uint32_t apart = 0;
+  asm volatile("" : "+v"(apart));  // lanes read each other's rows: no read moves across the writes
+  const uint8_t* ar = al + apart;
+  const uint32_t r8 = (uint32_t)lane >> 3, mine = r8 * ld + (lane & 7) * 16;
+
+  v4u ab[D][2], wb[D][2];
+  float as[D], ws[D];
+  auto load = [&](int s, int step) {
+    const uint32_t at = step < s1 ? (uint32_t)step * kStep : kOutside, sc = step < s1 ? 4u * (uint32_t)step : kOutside;
+    wb[s][0] = __builtin_amdgcn_raw_buffer_load_b128(rw0, (int)(mine + at), 0, 0);
+    wb[s][1] = __builtin_amdgcn_raw_buffer_load_b128(rw1, (int)(mine + at), 0, 0);
+    ab[s][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(mine + at), 0, 0);
+    ab[s][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(mine + 8 * ld + at), 0, 0);
+    as[s] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (int)(4u * (uint32_t)(lo * kb) + sc), 0, 0));
+    ws[s] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, (int)(my_block + sc), 0, 0));
+  };
+  auto store = [&](int s) {
+    const uint32_t at = r8 * kStep + (((lane & 7) ^ r8) & 7) * 16;
+    *reinterpret_cast<v4u*>(al + at) = ab[s][0];
+    *reinterpret_cast<v4u*>(al + 8 * kStep + at) = ab[s][1];
+    *reinterpret_cast<v4u*>(al + PART + at) = wb[s][0];
+    *reinterpret_cast<v4u*>(al + PART + 8 * kStep + at) = wb[s][1];
+  };
+  auto chunk = [&](int part, int c) {
+    return fp8_to_bf16(*reinterpret_cast<const v4u*>(ar + part + lo * kStep + ((c ^ lo) & 7) * 16));
+  };
+  f32x4 acc = {0, 0, 0, 0};
+#pragma unroll
+  for (int s = 0; s < D; ++s) load(s, s0 + s);
+  for (int k = s0; k < s1; k += D) {
+#pragma unroll
+    for (int s = 0; s < D; ++s) {
+      if (k + s < s1) {
+        store(s);
+        const float sc = as[s] * ws[s];
+        load(s, k + s + D);
+        f32x4 p = {0, 0, 0, 0};
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+          const Bf16x16 a = chunk(0, 4 * j + hi), w = chunk(PART, 4 * j + hi);
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.lo, a.lo, p, 0, 0, 0);
+          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.hi, a.hi, p, 0, 0, 0);
+        }
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(sc, p[r], acc[r]);
+      }
+    }
+  }
+  // the wavefronts' sums meet: lane l holds W rows 4 (l / 16) + r of row l % 16
+  __syncthreads();
+  float* sums = reinterpret_cast<float*>(pool);
+  *reinterpret_cast<f32x4*>(sums + wave * 256 + lo * 16 + 4 * hi) = acc;
+  __syncthreads();
+  const int t = threadIdx.x;
+  if (t < 16 * COLS) {
+    const int r = t / COLS, c = t % COLS;
+    float v = 0.0f, u = 0.0f;
+#pragma unroll
+    for (int w = 0; w < WAVES; ++w) {
+      v += sums[w * 256 + r * 16 + c];
+      if (GATED) u += sums[w * 256 + r * 16 + 8 + c];
+    }
+    if (GATED) v = silu_mul(v, u);
+    if (r < rows) {
+      const uint64_t to = (uint64_t)(row0 + r) * P.n + col0 + c;
+      if (MODE == kPlain && P.addend) v += P.addend[to];
+      if (MODE == kValues) P.partial[to] = v;
+      else if (MODE == kPlain && P.out_type == kOutFp32) reinterpret_cast<float*>(P.out)[to] = v;
+      else reinterpret_cast<uint16_t*>(P.out)[to] = (uint16_t)bf16_pair(v, 0.0f);
+    }
+  }
+}
+
 // The partial sums of `splits` runs of k to outputs: a thread has four columns
 // of a row, 32 of them a block of 128 columns.
 __global__ void __launch_bounds__(256) dense_finish_kernel(const DenseParams P, int splits) {
@@ -282,6 +386,25 @@ __global__ void __launch_bounds__(256) dense_finish_kernel(const DenseParams P, 
     *reinterpret_cast<uint2*>(P.out + 2 * to) = make_uint2(bf16_pair(v[0], v[1]), bf16_pair(v[2], v[3]));
 }
 
+hipError_t launch_finish(const DenseParams& p, int splits, hipStream_t stream) {
+  const int64_t threads = (int64_t)p.m * ((p.n + 127) / 128) * 32;
+  dense_finish_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(p, splits);
+  return hipGetLastError();
+}
+
+template <int WAVES, int D>
+hipError_t launch_few(const DenseParams& p, hipStream_t stream) {
+  const unsigned blocks = (unsigned)((p.m + 15) / 16 * (p.n / (p.gated ? 8 : 16)));
+  if (!p.gated) dense_few_kernel<WAVES, D, kPlain><<<blocks, WAVES * 64, 0, stream>>>(p);
+  else if (p.out_type == kOutFp8) dense_few_kernel<WAVES, D, kValues><<<blocks, WAVES * 64, 0, stream>>>(p);
+  else dense_few_kernel<WAVES, D, kGated><<<blocks, WAVES * 64, 0, stream>>>(p);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || p.out_type != kOutFp8) return e;
+  DenseParams q = p;
+  q.gated = 0;  // the values are already one each
+  return launch_finish(q, 1, stream);
+}
+
 // Through partial sums in the workspace, which they fit.
 template <int WM, int WN, int FM, int FN, int STAGES>
 hipError_t launch_split(const DenseParams& p, int splits, hipStream_t stream) {
@@ -291,9 +414,7 @@ hipError_t launch_split(const DenseParams& p, int splits, hipStream_t stream) {
   dense_kernel<WM, WN, FM, FN, STAGES, kPartial><<<(unsigned)tiles, WM * WN * 64, 0, stream>>>(p, splits);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
-  const int64_t threads = (int64_t)p.m * ((p.n + 127) / 128) * 32;
-  dense_finish_kernel<<<(unsigned)((threads + 255) / 256), 256, 0, stream>>>(p, splits);
-  return hipGetLastError();
+  return launch_finish(p, splits, stream);
 }
 
 // The product of `rows` rows from row `first` on.
@@ -327,35 +448,53 @@ hipError_t launch(const DenseParams& p, hipStream_t stream) {
 
 }  // namespace
 
+// Which tiles, and how many runs of k, by the sizes. The figures are us of
+// one call, its weights out of the caches, gated to fp8 with n 2048 and k 7168
+// | plain, to fp32 with an addend, with n 7168 and k 2048, unless said otherwise.
 hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   if (p.m == 0) return hipSuccess;
   const int64_t rows_w = p.gated ? 2 * (int64_t)p.n : p.n, kb = p.k / 128;
   const int64_t bytes = (int64_t)p.m * rows_w * 4;  // of one set of partial sums
-  // Runs of k for tiles of bm x bn of which `room` are under way at once: as
-  // many as there is room for, of 7 steps or more.
-  auto runs = [&](int64_t bm, int64_t bn, int64_t room) {
+  // Runs of k for tiles of bm x bn: as many as `room` workgroups allow, of 7
+  // steps or more, and `least` if there are so many steps.
+  auto runs = [&](int64_t bm, int64_t bn, int64_t room, int64_t least) {
     const int64_t tiles = (rows_w + bn - 1) / bn * ((p.m + bm - 1) / bm);
     int64_t s = room / tiles;
+    if (s < least) s = least;
     if (s > kb / 7) s = kb / 7;
     if (s > kWorkspace / bytes) s = kWorkspace / bytes;
     return s < 1 ? 1 : s;
   };
-  if (p.m <= kFewTokens) {
-    const int64_t s = runs(16, 64, 256);
+  // 16 x 16 while those are few: to bf16 1 row 8.4 (16 x 64 tiles in four runs
+  // of k 11.7), 32 rows 13.8 (16.0), 48 rows 17.9 (15.6 in 64 x 64); | 1 row 6.0
+  // (7.0), 32 rows 10.0 (7.7). To fp8 the second kernel is needed all the same:
+  // 1 row 10.9 (12.0), with n and k 4096 11.9 (11.1).
+  const int64_t few = ((int64_t)p.m + 15) / 16 * (p.n / (p.gated ? 8 : 16));
+  if (few <= (p.out_type == kOutFp8 ? kFewToFp8 : kFew)) return launch_few<16, 1>(p, stream);
+  // 16 x 64: n and k 4096, gated, 1 row 11.1 in two runs (14.4 in one, 64 x 64
+  // 13.9); | 32 rows 7.7 (64 x 64 10.9)
+  if (p.m <= (p.gated ? kTokens16Gated : kTokens16)) {
+    const int64_t s = runs(16, 64, 256, p.gated ? 2 : 1);
     if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<1, 4, 1, 1, 4>(p, (int)s, stream);
     return launch<1, 4, 1, 1, 4, kPlain>(p, stream);
   }
-  if (p.m <= (p.gated ? kSomeGatedTokens : kSomeTokens)) {
-    const int64_t s = runs(64, 64, 256);
+  // 64 x 64: 64 rows 16.8 (16 x 64 24.1), 128 rows 21.9 (128 x 128 23.9) | 11.3
+  // and 11.9 (128 x 128 15.6 in two runs), 256 rows 32 (29) | 18.2 (23.5)
+  if (p.m <= (p.gated ? kTokens64Gated : kTokens64)) {
+    const int64_t s = runs(64, 64, 256, 1);
     if ((p.gated && bytes <= kWorkspace) || kb - kb / s >= kWorthSplit)
       return launch_split<2, 2, 2, 2, 4>(p, (int)s, stream);
     if (!p.gated) return launch<2, 2, 2, 2, 4, kPlain>(p, stream);
   }
-  if (bytes <= kWorkspace && p.m <= kManyTokens) {
-    const int64_t s = runs(128, 128, 512);
+  // 128 x 128, two workgroups a CU: 777 rows 62 in two runs (71 in one, 128 x
+  // 256 68 to 107) | 36 (128 x 256 42, 64 x 64 and less 62); 8192 rows | 239
+  // (256 x 256 250)
+  if (bytes <= kWorkspace && p.m <= kTokens128) {
+    const int64_t s = runs(128, 128, 512, 1);
     if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<2, 2, 4, 4, 2>(p, (int)s, stream);
   }
   if (!p.gated) return launch<2, 2, 4, 4, 2, kPlain>(p, stream);
+  // 256 x 256: 8192 rows 412 (128 x 256 480), to bf16 400 (128 x 128 422)
   return p.out_type == kOutFp8 ? launch<4, 2, 4, 8, 2, kGatedFp8>(p, stream)
                                : launch<4, 2, 4, 8, 2, kGated>(p, stream);
 }
