@@ -253,3 +253,46 @@ def test_groups_within_32_bit_rounding(e, groups, topk_groups, best, with_bias):
     x = torch.from_numpy(rows).to(DEV)
     b = torch.from_numpy(bias).to(DEV) if with_bias else None
     verify(x, min(4, topk_groups * per), True, b, groups, topk_groups, best, True, 1.0)
+
+
+@pytest.mark.parametrize("e,groups,topk_groups", [(64, 8, 3), (256, 8, 4), (256, 16, 5), (48, 4, 2), (32, 2, 1)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_groups_of_one_value(e, groups, topk_groups, best, sigmoid):
+    """Groups whose best values are the same numbers, each once in its group:
+    those of a smaller number stay."""
+    g = torch.Generator(device=DEV).manual_seed(e + groups)
+    per = e // groups
+    x = -2.0 - torch.rand(40, e, generator=g, device=DEV)
+    at = torch.rand(40, groups, per, generator=g, device=DEV).argsort(2) + torch.arange(groups, device=DEV)[:, None] * per
+    for t in range(40):
+        level = torch.randint(0, 3, (groups,), generator=g, device=DEV).float()  # three values for all groups
+        x[t, at[t, :, 0]] = 1.0 + level / 4
+        x[t, at[t, :, 1]] = 0.5 - level / 4 if t % 2 else 0.5 * torch.ones_like(level)
+    for bias in (torch.zeros(e, device=DEV), torch.full((e,), 0.125, device=DEV), None):
+        verify(x, 4, sigmoid, bias, groups, topk_groups, best)
+        verify(x.bfloat16(), 4, sigmoid, bias, groups, topk_groups, best)
+
+
+@pytest.mark.parametrize("best", [1, 2])
+def test_groups_whose_values_and_members_are_near(best):
+    """Scores of exactly 1/2 and biases, so that values are exact: members and
+    groups some 1e-6 apart, in clusters of up to some 1e-5."""
+    rng = np.random.default_rng(8)
+    for t in range(60):
+        wide = (2e-6, 6e-6, 2e-5)[t % 3]
+        v = 0.2 + rng.uniform(-wide, wide, 64)
+        v[rng.random(64) < 0.6] = 0.1  # a few members each
+        b = torch.from_numpy((v - 0.5).astype(np.float32)).to(DEV)
+        verify(torch.zeros(3, 64, device=DEV), 4, True, b, 4, 2, best)
+    # one group clearly best, by less than what its two nearest members differ
+    off = 2.0 ** -19 + 0.6 * 2.0 ** -20
+    for above in np.arange(0.6, 2.6, 0.1):
+        v = np.full((4, 16), 0.05)
+        v[0, :3] = 0.3 - 0.9 * off * np.arange(3)
+        total = v[0, 0] + (v[0, 1] if best == 2 else 0.0) - above * off
+        for g, (first, less) in enumerate(((0.31, 0.0), (0.29, 0.4), (0.2, 40.0)), 1):
+            v[g, 5] = first if best == 2 else total - less * off
+            v[g, 6] = total - less * off - first if best == 2 else 0.01
+        b = torch.from_numpy((v.ravel() - 0.5).astype(np.float32)).to(DEV)
+        verify(torch.zeros(2, 64, device=DEV), 4, True, b, 4, 2, best)
