@@ -37,30 +37,36 @@ __device__ __forceinline__ uint32_t opaque_zero() {
   return zero;
 }
 
-// Eight fp32 in three bf16 parts of 8 bits, by cutting: the parts' signs and
+// Four fp32 in three bf16 parts of 8 bits, by cutting: the parts' signs and
 // exponents are the value's own, so nothing overflows, and what is left after
 // each cut is exact.
+struct Parts4 {
+  v2u part[3];
+};
+__device__ __forceinline__ Parts4 cut(v4u v) {
+  float f[4];
+#pragma unroll
+  for (int i = 0; i < 4; ++i) f[i] = __uint_as_float(v[i]);
+  Parts4 o;
+#pragma unroll
+  for (int p = 0; p < 3; ++p) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+      o.part[p][i] = __builtin_amdgcn_perm(__float_as_uint(f[2 * i + 1]), __float_as_uint(f[2 * i]), 0x07060302u);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] -= __uint_as_float(__float_as_uint(f[i]) & 0xFFFF0000u);
+  }
+  return o;
+}
 struct Parts {
   bf16x8 part[3];
 };
 __device__ __forceinline__ Parts cut(v4u a, v4u b) {
-  float f[8];
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    f[i] = __uint_as_float(a[i]);
-    f[4 + i] = __uint_as_float(b[i]);
-  }
+  const Parts4 x = cut(a), y = cut(b);
   Parts o;
 #pragma unroll
-  for (int p = 0; p < 3; ++p) {
-    v4u packed;
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-      packed[i] = __builtin_amdgcn_perm(__float_as_uint(f[2 * i + 1]), __float_as_uint(f[2 * i]), 0x07060302u);
-    o.part[p] = __builtin_bit_cast(bf16x8, packed);
-#pragma unroll
-    for (int i = 0; i < 8; ++i) f[i] -= __uint_as_float(__float_as_uint(f[i]) & 0xFFFF0000u);
-  }
+  for (int p = 0; p < 3; ++p)
+    o.part[p] = __builtin_bit_cast(bf16x8, v4u{x.part[p][0], x.part[p][1], y.part[p][0], y.part[p][1]});
   return o;
 }
 
@@ -119,11 +125,13 @@ __global__ void __launch_bounds__(64) gate_row_kernel(const GateParams P) {
   }
 }
 
-// 16 tokens x EW experts (16, or 8 where that gives the GPU more to do at once).
+// 16 tokens x EW experts (as few as the GPU has room for). fp32 weights are
+// cut on their way into LDS, once each (cut as fragments, whose 16 rows repeat
+// the EW, 128 tokens by 256 experts took 11.2 us).
 template <bool FP32, int EW, int WAVES, int D>
 __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P) {
   constexpr int ITEM = FP32 ? 4 : 2, WROW = kColumns * ITEM, WL = (EW * WROW + 1023) / 1024;
-  constexpr int XPART = 16 * 128, WPART = EW * WROW;
+  constexpr int XPART = 16 * 128, PARTS = FP32 ? 3 : 1, WPART = PARTS * EW * 128;
   __shared__ __align__(16) uint8_t pool[WAVES * (XPART + WPART)];
   const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -172,26 +180,29 @@ __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P
       for (int i = 0; i < WL; ++i) {
         constexpr int CH = WROW / 16;
         const int r = lane / CH + 64 / CH * i, c = lane % CH;
-        if (64 / CH <= EW || r < EW) *reinterpret_cast<v4u*>(wl + r * WROW + ((c ^ r) & (CH - 1)) * 16) = wb[s][i];
+        if (64 / CH > EW && r >= EW) continue;
+        if constexpr (FP32) {
+          const Parts4 v = cut(wb[s][i]);
+#pragma unroll
+          for (int p = 0; p < 3; ++p)
+            *reinterpret_cast<v2u*>(wl + (p * EW + r) * 128 + ((c / 2 ^ r) & 7) * 16 + (c & 1) * 8) = v.part[p];
+        } else {
+          *reinterpret_cast<v4u*>(wl + r * 128 + ((c ^ r) & 7) * 16) = wb[s][i];
+        }
       }
     };
-    auto chunk = [&](const uint8_t* from, int r, int row_bytes, int c) {
-      return *reinterpret_cast<const v4u*>(from + r * row_bytes + ((c ^ r) & (row_bytes / 16 - 1)) * 16);
+    auto chunk = [&](const uint8_t* from, int r, int c) {
+      return __builtin_bit_cast(bf16x8, *reinterpret_cast<const v4u*>(from + r * 128 + ((c ^ r) & 7) * 16));
     };
     const int wrow = lo & (EW - 1);
     f32x4 acc = {0, 0, 0, 0};
     auto multiply = [&] {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
-        const bf16x8 a = __builtin_bit_cast(bf16x8, chunk(xr, lo, 128, 4 * j + hi));
-        if constexpr (FP32) {
-          const Parts w = cut(chunk(wr, wrow, WROW, 8 * j + 2 * hi), chunk(wr, wrow, WROW, 8 * j + 2 * hi + 1));
+        const bf16x8 a = chunk(xr, lo, 4 * j + hi);
 #pragma unroll
-          for (int p = 0; p < 3; ++p) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.part[p], a, acc, 0, 0, 0);
-        } else {
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, chunk(wr, wrow, WROW, 4 * j + hi)), a,
-                                                        acc, 0, 0, 0);
-        }
+        for (int p = 0; p < PARTS; ++p)
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(chunk(wr + p * EW * 128, wrow, 4 * j + hi), a, acc, 0, 0, 0);
       }
     };
 #pragma unroll
@@ -380,9 +391,10 @@ hipError_t launch_row(const GateParams& p, hipStream_t stream) {
 // Which kernel, by the sizes (us at hidden 7168 and 256 experts, weights bf16 |
 // fp32). Up to kRowTokens tokens: a wavefront an expert (1 token 3.5 | 4.2, where
 // 16 x 8 take 6.0 | 9.6; 4 tokens 6.1 | 6.5 against 6.0 | 9.8). Then 16 tokens
-// by as few experts as fill the GPU once (64 tokens: 16 x 4 6.8 | 9.6, 16 x 8 6.8 |
-// 10.6, 16 x 16 8.3 | 12.7), up to as many logits as tiles do faster (768
-// tokens 19.7 against 21.3, 1024 tokens 31 against 24 | 46 against 48). Then the
+// by as few experts as fill the GPU once (64 tokens: 16 x 4 6.8 | 8.6, 16 x 8 6.8 |
+// 10.0, 16 x 16 8.3 | 12.7; 128 tokens 16 x 8 7.2 | 10.5; 256 tokens 16 x 16 9.1 |
+// 13.7), up to as many logits as tiles do faster (768 tokens 19.2 against 21.3,
+// 1024 tokens 31 against 24 | 46 against 48). Then the
 // smallest tiles that are not too many: 64 x 32 (2048 tokens 29 | 49, in 64 x 64
 // 34 | 79; 4096 tokens 49 | 75), bf16 64 x 64 (4096 tokens 36, 8192 63; in
 // 128 x 128 67, 69), fp32 128 x 32 (8192 tokens 110, in 64 x 32 141), 128 x 64
