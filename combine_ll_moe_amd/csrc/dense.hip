@@ -9,10 +9,20 @@
 //
 // Design: a workgroup's wavefronts take a tile of rows by weight rows; a k step is 128
 // bytes of every row, copied from memory straight into LDS some steps ahead
-// of the products. A row's eight 16-byte chunks are permuted by the row's low
-// bits, so that the 16 lanes that read one chunk of 16 rows meet no bank twice.
-// Rows behind m or n and steps behind k are outside the buffer descriptors:
-// zeros.
+// of the products, the scales with it. A row's eight 16-byte chunks are
+// permuted by the row's low bits, so that the 16 lanes that read one chunk of
+// 16 rows meet no bank twice. Rows behind m or n and steps behind k are outside
+// the buffer descriptors: zeros. Where tiles alone do not fill the GPU, runs of
+// k go to workgroups of their own, whose sums meet in the workspace and are
+// finished by a second kernel; few rows have a kernel that needs no second one
+// (launch_dense says which sizes take which).
+//
+// Bound: few rows are latency and a second launch (one row, gated, n 2048, k
+// 7168, 29 MB: 8.4 us to bf16, 10.9 to fp8, of which 2.0 are the second
+// kernel and the rest its launch). Many rows: 8192 x 4096 x 7168 take 400 us, 1.2 PFLOP/s; the copies
+// alone take 203 of them and the products without copies 340, which overlap no
+// better: a SIMD's matrix unit is busy 52 % of the time, and 2.8 vector
+// instructions a product (conversion and scaling) share its wavefronts' issue.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -27,12 +37,15 @@ namespace {
 enum : int { kPartial = 0, kPlain = 1, kGated = 2, kGatedFp8 = 3 };
 static_assert(kStep == kFp8Block);  // a k step is one scale's columns
 constexpr int64_t kWorkspace = LL_MOE_DENSE_WORKSPACE;
-// Workgroups up to which there are enough of 16 x 16; rows up to which a tile
-// has 16, 64 and 128 of them; steps of k that a split has to save, to be worth
-// its second kernel (1 row, n 7168, k 2048: 7.2 us, in two runs 8.2; 17 rows, n
-// 1040, k 4096: 10.4 us, in four runs 8.0).
+// Up to so many workgroups there are 16 x 16 tiles, and up to so many tiles 64 x
+// 64 ones, with more or fewer steps of k than kDeep; rows up to which a tile has
+// 16, 64 and 128 of them all the same; steps of k that a split has to save, to be
+// worth its second kernel (17 rows, n 1040, k 4096: 10.4 us, in four runs 8.0; 1
+// row, n 7168, k 2048: 7.2, in two 8.2).
 constexpr int kFew = 512, kFewToFp8 = 256;
-constexpr int kTokens16 = 32, kTokens16Gated = 16, kTokens64 = 256, kTokens64Gated = 128, kTokens128 = 4096;
+constexpr int kDeep = 40, kTiles64 = 512, kTiles64Deep = 256;
+constexpr int kDeepGated = 24, kTiles64Gated = 256, kTiles64GatedDeep = 128;
+constexpr int kTokens16 = 32, kTokens16Gated = 16, kTokens64 = 64, kTokens128 = 4096;
 constexpr int kWorthSplit = 12;
 
 // WM x WN wavefronts, each FM x FN fragments of 16 x 16; STAGES buffers of a
@@ -47,14 +60,13 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams
   constexpr int SCALES = (BM + BN) * kStep;  // in a stage: 512 bytes of scales a wavefront
   constexpr int STAGE = SCALES + WAVES * 512;
   static_assert(FM <= 4);
-  static_assert(STAGES >= 2 && STAGES <= 6);
+  static_assert(STAGES >= 2 && STAGES <= 4);
   static_assert(WI % WAVES == 0 && (AI % WAVES == 0 || WAVES % AI == 0) && (!GATED || WI / 2 % WAVES == 0));
   static_assert(FN * 16 <= 128 && (MODE != kGatedFp8 || BN == 256));
   // an array each, so that the compiler can tell a step's copies from the
   // reads of another one's
   __shared__ __align__(16) uint8_t st0[STAGE], st1[STAGE];
   __shared__ __align__(16) uint8_t st2[STAGES > 2 ? STAGE : 16], st3[STAGES > 3 ? STAGE : 16];
-  __shared__ __align__(16) uint8_t st4[STAGES > 4 ? STAGE : 16], st5[STAGES > 5 ? STAGE : 16];
   const int tid = threadIdx.x, lane = tid & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave / WN, wn = wave % WN;
@@ -169,7 +181,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams
   // way, then all wavefronts meet: the step is whole, and the buffer of the one
   // before it is free for the step STAGES - 1 ahead.
   constexpr int AHEAD = STAGES - 1;
-  uint8_t* const buffers[6] = {st0, st1, st2, st3, st4, st5};
+  uint8_t* const buffers[4] = {st0, st1, st2, st3};
 #pragma unroll
   for (int s = 0; s < AHEAD; ++s) fetch(k0 + s, buffers[s]);
   // Steps behind k1 are zeros: whole rounds of STAGES, without branches.
@@ -455,11 +467,11 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   if (p.m == 0) return hipSuccess;
   const int64_t rows_w = p.gated ? 2 * (int64_t)p.n : p.n, kb = p.k / 128;
   const int64_t bytes = (int64_t)p.m * rows_w * 4;  // of one set of partial sums
-  // Runs of k for tiles of bm x bn: as many as `room` workgroups allow, of 7
+  auto tiles = [&](int64_t bm, int64_t bn) { return (rows_w + bn - 1) / bn * ((p.m + bm - 1) / bm); };
+  // Runs of k for so many tiles: as many as `room` workgroups allow, of 7
   // steps or more, and `least` if there are so many steps.
-  auto runs = [&](int64_t bm, int64_t bn, int64_t room, int64_t least) {
-    const int64_t tiles = (rows_w + bn - 1) / bn * ((p.m + bm - 1) / bm);
-    int64_t s = room / tiles;
+  auto runs = [&](int64_t n, int64_t room, int64_t least) {
+    int64_t s = room / n;
     if (s < least) s = least;
     if (s > kb / 7) s = kb / 7;
     if (s > kWorkspace / bytes) s = kWorkspace / bytes;
@@ -467,21 +479,26 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   };
   // 16 x 16 while those are few: to bf16 1 row 8.4 (16 x 64 tiles in four runs
   // of k 11.7), 32 rows 13.8 (16.0), 48 rows 17.9 (15.6 in 64 x 64); | 1 row 6.0
-  // (7.0), 32 rows 10.0 (7.7). To fp8 the second kernel is needed all the same:
-  // 1 row 10.9 (12.0), with n and k 4096 11.9 (11.1).
+  // (7.0), 32 rows 10.0 (7.7); 512 rows, n 256, k 2048, to bf16 5.8 (64 x 64
+  // 9.1). To fp8 the second kernel is needed all the same: 1 row 10.9 (12.0),
+  // with n and k 4096 11.9 (11.1).
   const int64_t few = ((int64_t)p.m + 15) / 16 * (p.n / (p.gated ? 8 : 16));
   if (few <= (p.out_type == kOutFp8 ? kFewToFp8 : kFew)) return launch_few<16, 1>(p, stream);
   // 16 x 64: n and k 4096, gated, 1 row 11.1 in two runs (14.4 in one, 64 x 64
   // 13.9); | 32 rows 7.7 (64 x 64 10.9)
-  if (p.m <= (p.gated ? kTokens16Gated : kTokens16)) {
-    const int64_t s = runs(16, 64, 256, p.gated ? 2 : 1);
-    if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<1, 4, 1, 1, 4>(p, (int)s, stream);
-    return launch<1, 4, 1, 1, 4, kPlain>(p, stream);
-  }
+  if (p.gated && p.m <= kTokens16Gated)
+    return launch_split<1, 4, 1, 1, 4>(p, (int)runs(tiles(16, 64), 256, 2), stream);
+  if (!p.gated && p.m <= kTokens16) return launch<1, 4, 1, 1, 4, kPlain>(p, stream);
   // 64 x 64: 64 rows 16.8 (16 x 64 24.1), 128 rows 21.9 (128 x 128 23.9) | 11.3
-  // and 11.9 (128 x 128 15.6 in two runs), 256 rows 32 (29) | 18.2 (23.5)
-  if (p.m <= (p.gated ? kTokens64Gated : kTokens64)) {
-    const int64_t s = runs(64, 64, 256, 1);
+  // and 11.9 (128 x 128 15.6 in two runs), 256 rows 32 (29) | 18.2 (23.5). To
+  // bf16, plain, n 2048: 512 rows, k 2048 10.7 (128 x 128 19.1), k 7168 30.4
+  // (29.5); 1024 rows, k 2048 17.3 (21.4), k 7168 50.4 (43.8). Gated, n 1024: 256
+  // rows, k 1024 9.5 (13.2), k 7168 21.5 (26.3); 512 rows, k 1024 11.3 (15.4), k
+  // 7168 31.8 (30.0)
+  const int64_t most64 = p.gated ? (kb > kDeepGated ? kTiles64GatedDeep : kTiles64Gated)
+                                 : (kb > kDeep ? kTiles64Deep : kTiles64);
+  if (p.m <= kTokens64 || tiles(64, 64) <= most64) {
+    const int64_t s = runs(tiles(64, 64), 256, 1);
     if ((p.gated && bytes <= kWorkspace) || kb - kb / s >= kWorthSplit)
       return launch_split<2, 2, 2, 2, 4>(p, (int)s, stream);
     if (!p.gated) return launch<2, 2, 2, 2, 4, kPlain>(p, stream);
@@ -490,7 +507,7 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   // 256 68 to 107) | 36 (128 x 256 42, 64 x 64 and less 62); 8192 rows | 239
   // (256 x 256 250)
   if (bytes <= kWorkspace && p.m <= kTokens128) {
-    const int64_t s = runs(128, 128, 512, 1);
+    const int64_t s = runs(tiles(128, 128), 512, 1);
     if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<2, 2, 4, 4, 2>(p, (int)s, stream);
   }
   if (!p.gated) return launch<2, 2, 4, 4, 2, kPlain>(p, stream);
