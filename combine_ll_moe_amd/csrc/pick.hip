@@ -22,7 +22,7 @@
 // values that can be among the picks meet in LDS to be ranked. fp32 values
 // decide wherever they are further apart than they may be off; those that are
 // not are taken again to 1e-10, and a row that this does not settle (equal
-// groups, more than 16 equal values) is done by a whole wavefront in 64 bits
+// groups, more than 16 near values of scores with a bias) is done by a whole wavefront in 64 bits
 // (exact_row), as is every row of the other counts of experts and groups.
 //
 // Bound: 16384 tokens of 256 experts (fp32, sigmoid with a bias, 8 groups, 4
@@ -89,6 +89,18 @@ __device__ __forceinline__ double row_sum(double v) {
   v += dpp<kRor + 4>(v);
   v += dpp<kRor + 2>(v);
   return v + dpp<kRor + 1>(v);
+}
+
+__device__ __forceinline__ uint64_t row_max(uint64_t v) {
+  auto with = [&](uint32_t hi, uint32_t lo) {
+    const uint64_t other = (uint64_t)hi << 32 | lo;
+    v = other > v ? other : v;
+  };
+  with(dpp<kRor + 8>((uint32_t)(v >> 32)), dpp<kRor + 8>((uint32_t)v));
+  with(dpp<kRor + 4>((uint32_t)(v >> 32)), dpp<kRor + 4>((uint32_t)v));
+  with(dpp<kRor + 2>((uint32_t)(v >> 32)), dpp<kRor + 2>((uint32_t)v));
+  with(dpp<kRor + 1>((uint32_t)(v >> 32)), dpp<kRor + 1>((uint32_t)v));
+  return v;
 }
 
 // How many of a row's 16 values are larger.
@@ -543,7 +555,22 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
         if (SCORED) found_l[wave][sub][at] = l[i];
         ++at;
       }
-    unsure |= all > 16;
+    uint64_t many = 0;  // lane k: pick k, where there are more than 16
+    if constexpr (SCORED) {
+      unsure |= all > 16;
+    } else if (__ballot(all > 16)) {
+      uint64_t last = ~0ull;
+      for (int k = 0; k < P.topk; ++k) {
+        uint64_t next = 0;
+#pragma unroll
+        for (int i = 0; i < V; ++i) {
+          const uint64_t v = (uint64_t)ordered(key[i]) << 32 | (0xFFFFu - expert(i));
+          if (key[i] > none32 && v < last && v > next) next = v;
+        }
+        last = row_max(next);
+        if (l16 == k) many = last;
+      }
+    }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
     const bool in = (uint32_t)l16 < all;
@@ -560,10 +587,11 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
     }
     __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
     __builtin_amdgcn_wave_barrier();
-    const uint64_t pick = in ? found[wave][sub][l16] : 0;
+    uint64_t pick = in ? found[wave][sub][l16] : 0;
+    if (!SCORED && all > 16) pick = many;
     const float pick_key = unordered((uint32_t)(pick >> 32));
     float pick_l = !SCORED ? pick_key : in ? found_l[wave][sub][l16] : 0.0f;
-    int e = in ? (int)(0xFFFFu - (uint32_t)pick) : -1;
+    int e = pick ? (int)(0xFFFFu - (uint32_t)pick) : -1;
     if constexpr (SCORED) {
       // neighbours too near to tell
       const float next = dpp<kShl + 1>(pick_key);

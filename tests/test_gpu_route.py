@@ -296,3 +296,20 @@ def test_groups_whose_values_and_members_are_near(best):
             v[g, 6] = total - less * off - first if best == 2 else 0.01
         b = torch.from_numpy((v.ravel() - 0.5).astype(np.float32)).to(DEV)
         verify(torch.zeros(2, 64, device=DEV), 4, True, b, 4, 2, best)
+
+
+@pytest.mark.parametrize("e,groups,topk_groups", [(64, 1, 1), (256, 1, 1), (256, 8, 4), (161, 1, 1), (512, 1, 1), (128, 2, 1)])
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_rows_of_many_equal_logits(e, groups, topk_groups, sigmoid):
+    """Rows of zeros (tokens of padding), of two values, of a few above many."""
+    g = torch.Generator(device=DEV).manual_seed(e)
+    x = torch.randn(41, e, generator=g, device=DEV)
+    x[1::4] = 0.0
+    x[2::8] = x[2::8].round()
+    x[3::8] = (x[3::8] > 1.5).float()
+    x[6::8] = x[6::8].clamp(max=0.3)
+    x[7, : e // 2] = -INF
+    x[5, 20:] = -INF
+    for topk in (1, 3, 8, 16):
+        for dtype in (torch.float32, torch.bfloat16):
+            verify(x.to(dtype), topk, sigmoid, None, groups, topk_groups, 1, topk == 8)
