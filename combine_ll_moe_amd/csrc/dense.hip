@@ -195,6 +195,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams
       multiply(buffers[s]);
     }
   }
+  wait_loads<0>();  // no copy is under way when the LDS is another workgroup's
 
   constexpr int F = GATED ? FN / 2 : FN;
   if constexpr (GATED) {
@@ -207,8 +208,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams
   }
   float* amaxes = reinterpret_cast<float*>(st0);  // fp8: amax of a row's part, [BM][WN]
   if constexpr (MODE == kGatedFp8) {
-    wait_loads<0>();
-    __syncthreads();  // copies behind the last step have landed
+    __syncthreads();  // copies behind the last step have landed, of all wavefronts
 #pragma unroll
     for (int m = 0; m < FM; ++m) {
       float v = 0.0f;

@@ -332,6 +332,7 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) gate_tile_kernel(const GatePar
       multiply(buffers[s]);
     }
   }
+  wait_loads<0>();  // no copy is under way when the LDS is another workgroup's
 #pragma unroll
   for (int m = 0; m < FM; ++m) {
     const int r = wm * FM * 16 + m * 16 + lo;
@@ -394,12 +395,11 @@ hipError_t launch_row(const GateParams& p, hipStream_t stream) {
 // by as few experts as fill the GPU once (64 tokens: 16 x 4 6.8 | 8.6, 16 x 8 6.8 |
 // 10.0, 16 x 16 8.3 | 12.7; 128 tokens 16 x 8 7.2 | 10.5; 256 tokens 16 x 16 9.1 |
 // 13.7), up to as many logits as tiles do faster (768 tokens 19.2 against 21.3,
-// 1024 tokens 31 against 24 | 46 against 48). Then the
-// smallest tiles that are not too many: 64 x 32 (2048 tokens 29 | 49, in 64 x 64
-// 34 | 79; 4096 tokens 49 | 75), bf16 64 x 64 (4096 tokens 36, 8192 63; in
-// 128 x 128 67, 69), fp32 128 x 32 (8192 tokens 110, in 64 x 32 141), 128 x 64
-// (16384 tokens 188, in 128 x 32 207), bf16 128 x 128 (16384 tokens 79, in 64 x
-// 64 118).
+// 1024 tokens 31 against 24 | 46 against 48). Then the smallest tiles that are
+// not too many: 64 x 32 (2048 tokens 29 | 49, in 64 x 64 34 | 79; 4096 tokens 49 |
+// 75), bf16 64 x 64 (4096 tokens 36, 8192 63; in 128 x 128 67, 69), fp32 128 x 32
+// (8192 tokens 110, in 64 x 32 141), 128 x 64 (16384 tokens 188, in 128 x 32 207),
+// bf16 128 x 128 (16384 tokens 79, in 64 x 64 118).
 hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   if (p.num_tokens == 0) return hipSuccess;
   auto tiles = [&](int64_t tokens, int64_t experts) {

@@ -468,8 +468,9 @@ int ll_moe_rms_norm(int num_tokens, int hidden, int x_dtype, int out_dtype, floa
  *   num_tokens >= 0 (0 enqueues nothing), hidden % 8 == 0, hidden <= 32768,
  *   num_experts <= 4096. logits may overlap neither input. A token's logits
  * are of its row and the weights alone (a NaN stays in its row); how a sum is
- * grouped goes by the sizes of the call. With fp32 weights an infinity in x,
- * or a weight that is not finite, gives NaN. Enqueued on `stream`.
+ * grouped goes by the sizes of the call. Where an infinity in x meets an fp32
+ * weight, or a value an fp32 weight that is not finite, the logit may be NaN
+ * instead of an infinity. Enqueued on `stream`.
  */
 int ll_moe_gate(int num_tokens, int hidden, int num_experts, int weight_dtype, const void* x,
                 const void* weight, float* logits, hipStream_t stream);
@@ -490,13 +491,13 @@ int ll_moe_gate(int num_tokens, int hidden, int num_experts, int weight_dtype, c
  * A logit that is NaN or -infinity leaves its expert out, of the picks and of
  * the softmax's sum; so does a bias that is, of the picks. A group that has
  * fewer than group_best experts left counts as -infinity. +infinity counts as
- * the largest fp32 (3.4e38). Where fewer than topk experts are left, the picks behind them are
- * -1 with weight 0, as are all picks of rows at or behind *num_valid: the
- * dispatch and the combine leave such entries out. Renormalised weights are
- * right where every picked score underflows, too.
+ * the largest fp32 (3.4e38). Where fewer than topk experts are left, the picks
+ * behind them are -1 with weight 0, as are all picks of rows at or behind
+ * *num_valid: the dispatch and the combine leave such entries out. Renormalised
+ * weights are right where every picked score underflows, too.
  *   logits_dtype: LL_MOE_FP32 or LL_MOE_BF16.
- *   logits:       device [num_tokens, num_experts], 16-byte aligned; rows
- *                 behind *num_valid are not read.
+ *   logits:       device [num_tokens, num_experts], 16-byte aligned; what
+ *                 rows at or behind *num_valid hold does not matter.
  *   bias:         device fp32 [num_experts], or NULL.
  *   num_valid:    device int32, or NULL: every row is valid. Read when the
  *                 call runs, so a captured call serves batches of any size.
