@@ -396,10 +396,11 @@ hipError_t launch_row(const GateParams& p, hipStream_t stream) {
 // 10.0, 16 x 16 8.3 | 12.7; 128 tokens 16 x 8 7.2 | 10.5; 256 tokens 16 x 16 9.1 |
 // 13.7), up to as many logits as tiles do faster (768 tokens 19.2 against 21.3,
 // 1024 tokens 31 against 24 | 46 against 48). Then the smallest tiles that are
-// not too many: 64 x 32 (2048 tokens 29 | 49, in 64 x 64 34 | 79; 4096 tokens 49 |
-// 75), bf16 64 x 64 (4096 tokens 36, 8192 63; in 128 x 128 67, 69), fp32 128 x 32
-// (8192 tokens 110, in 64 x 32 141), 128 x 64 (16384 tokens 188, in 128 x 32 207),
-// bf16 128 x 128 (16384 tokens 79, in 64 x 64 118).
+// not too many: 64 x 32 (2048 tokens 30 | 51, in 64 x 64 34 | 79; 4096 tokens 50 |
+// 77), then with bf16 64 x 64 (4096 tokens 36; 8192 63), 64 x 128, two a CU (4096
+// tokens 52, 8192 54, 10000 96), and 128 x 128 (8192 tokens 70, 10000 71, 16384
+// 78), with fp32 128 x 32 (4096 tokens 93, 8192 110, 16384 216) and 128 x 64
+// (8192 tokens 118, 16384 193).
 hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   if (p.num_tokens == 0) return hipSuccess;
   auto tiles = [&](int64_t tokens, int64_t experts) {
@@ -422,8 +423,9 @@ hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
     return tiles(16, 16) <= kCus ? launch_few<false, 16, 16, 2>(p, stream) : launch_few<false, 16, 8, 2>(p, stream);
   }
   if (tiles(64, 32) <= kCus) return launch_tile<false, 2, 2, 2, 1, 4>(p, stream);
-  return tiles(128, 128) < kCus * 3 / 4 ? launch_tile<false, 2, 2, 2, 2, 4>(p, stream)
-                                        : launch_tile<false, 2, 4, 4, 2, 4>(p, stream);
+  if (tiles(64, 64) <= kCus) return launch_tile<false, 2, 2, 2, 2, 4>(p, stream);
+  return tiles(64, 128) <= kCus ? launch_tile<false, 4, 2, 1, 4, 3>(p, stream)
+                                : launch_tile<false, 2, 4, 4, 2, 4>(p, stream);
 }
 
 }  // namespace llmoe
