@@ -667,6 +667,7 @@ hipError_t launch_pick(const PickParams& p, hipStream_t stream) {
     if (e == 512) return launch_rows<32, true>(p, stream);
     if (e <= 64) return launch_rows<4, false>(p, stream);
     if (e <= 128) return launch_rows<8, false>(p, stream);
+    if (e <= 192) return launch_rows<12, false>(p, stream);
     return e <= 256 ? launch_rows<16, false>(p, stream) : launch_rows<32, false>(p, stream);
   }
   if (e <= 64) return launch<1>(p, stream);
