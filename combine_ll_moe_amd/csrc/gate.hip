@@ -5,7 +5,8 @@
 // cut into three bf16 parts of 8 bits each, W = W0 + W1 + W2 exactly, and
 // three products share one fp32 sum: no bit of a weight is lost, where the
 // matrix cores have no fp32 product of this rate. (A weight that is not finite
-// has NaN for its rest.)
+// has NaN for its rest; of a tiny one, bits below 2^-133, bf16's smallest, are
+// left out, and a product sums subnormal values to some 17 bits.)
 //
 // Design, by how much work there is (launch_gate): a wavefront with one
 // expert's row (gate_row_kernel); 16 tokens by a few experts, whose columns are

@@ -460,7 +460,9 @@ int ll_moe_rms_norm(int num_tokens, int hidden, int x_dtype, int out_dtype, floa
 /*
  * ll_moe_gate - the router's logits.
  *   logits[t, e] = sum over c < hidden of x[t, c] * weight[e, c]
- * with exact products and fp32 sums (fp32 weights are not rounded).
+ * with exact products and fp32 sums (fp32 weights are not rounded). Of an fp32
+ * weight, bits below 2^-133 may not count; values below 2^-126 may count to 16
+ * bits only.
  *   weight_dtype: LL_MOE_BF16 or LL_MOE_FP32.
  *   x:       device bf16 [num_tokens, hidden], 16-byte aligned.
  *   weight:  device [num_experts, hidden], 16-byte aligned.

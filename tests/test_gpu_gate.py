@@ -108,3 +108,20 @@ def test_captured():
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(out, want)
+
+
+@pytest.mark.parametrize("t", [1, 4, 30, 200, 9000])
+@pytest.mark.parametrize("wtype", [BF16, F32])
+def test_tiny_values(t, wtype):
+    """Weights from 2^-100 to fp32's subnormals: an fp32 weight is off by less
+    than 2^-133, and a sum whose weights lie below 2^-126 by 2^-16 of its
+    magnitudes."""
+    g = torch.Generator(device=DEV).manual_seed(t)
+    for power in (-100, -115, -125, -130, -140):
+        x = (torch.randn(t, 64, generator=g, device=DEV) * 2.0 ** 90).to(BF16)
+        w = (torch.randn(48, 64, generator=g, device=DEV).double() * 2.0 ** power).to(wtype)
+        got = run(x, w).double()
+        p, bound = X.product(x.double(), w.double())
+        size = x.double().abs() @ w.double().abs().t()
+        bound = 3 * bound + x.double().abs().sum(1, keepdim=True) * 2.0 ** -133 * (wtype == F32) + size * 2.0 ** -16
+        assert bool(((got - p).abs() <= bound).all()), (power, ((got - p).abs() / bound).max().item())
