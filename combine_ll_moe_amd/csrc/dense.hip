@@ -486,7 +486,7 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   if (few <= (p.out_type == kOutFp8 ? kFewToFp8 : kFew)) return launch_few<16, 1>(p, stream);
   // 16 x 64: n and k 4096, gated, 1 row 11.1 in two runs (14.4 in one, 64 x 64
   // 13.9); | 32 rows 7.7 (64 x 64 10.9)
-  if (p.gated && p.m <= kTokens16Gated)
+  if (p.gated && p.m <= kTokens16Gated && bytes <= kWorkspace)
     return launch_split<1, 4, 1, 1, 4>(p, (int)runs(tiles(16, 64), 256, 2), stream);
   if (!p.gated && p.m <= kTokens16) return launch<1, 4, 1, 1, 4, kPlain>(p, stream);
   // 64 x 64: 64 rows 16.8 (16 x 64 24.1), 128 rows 21.9 (128 x 128 23.9) | 11.3

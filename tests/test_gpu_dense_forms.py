@@ -47,6 +47,19 @@ def test_sums_that_the_workspace_does_not_hold():
     verify(60, 147456, 128, True, BF16)
 
 
+@pytest.mark.parametrize("m,n,k,out", [(16, 524304, 128, BF16), (9, 1 << 20, 128, F8), (2, 1 << 20, 128, BF16)])
+def test_the_widest_weights_stay_inside_the_workspace(m, n, k, out):
+    a, a_s, w, w_s, _ = make(m, n, k, True, 4)
+    space = torch.full((ll.DENSE_WORKSPACE * 3,), 0x5A, dtype=torch.uint8, device=DEV)
+    o = torch.empty(m, n, device=DEV).to(out)
+    s = torch.empty(m, n // 128, device=DEV) if out == F8 else None
+    ll.ll_moe_dense_gemm(m, n, k, ll.ACT_SILU_MUL, ll.FP8_E4M3 if out == F8 else ll.BF16, a, a_s, w, w_s, None, o, s, space)
+    torch.cuda.synchronize()
+    assert bool((space[ll.DENSE_WORKSPACE:] == 0x5A).all())
+    del space
+    verify(m, n, k, True, out)
+
+
 @pytest.mark.parametrize("m,n,k,gated,out", [
     (5, 8208, 256, False, BF16), (40, 1392, 1920, True, BF16), (130, 1040, 7168, False, F32), (700, 1040, 896, True, BF16),
     (3000, 272, 1024, False, F32), (4100, 384, 256, True, F8), (100, 384, 3584, True, F8), (16, 256, 512, True, F8)])
