@@ -47,6 +47,7 @@ constexpr int kDeep = 40, kTiles64 = 512, kTiles64Deep = 256;
 constexpr int kDeepGated = 24, kTiles64Gated = 256, kTiles64GatedDeep = 128;
 constexpr int kTokens16 = 32, kTokens16Gated = 16, kTokens64 = 64, kTokens128 = 4096;
 constexpr int kWorthSplit = 12;
+constexpr int64_t kCus = 256;
 
 // WM x WN wavefronts, each FM x FN fragments of 16 x 16; STAGES buffers of a
 // step in LDS. The steps of k are divided among `splits` workgroups.
@@ -503,17 +504,29 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
       return launch_split<2, 2, 2, 2, 4>(p, (int)s, stream);
     if (!p.gated) return launch<2, 2, 2, 2, 4, kPlain>(p, stream);
   }
+  // Gated, many rows: 256 x 256, a tile a CU, as many rows as fill the CUs a
+  // whole number of times (8192 rows 412, in 128 x 256 480; to bf16 400, in 128 x
+  // 128 422). What is left goes by its own size, unless it nearly fills them too
+  // (3300 rows 195, in 128 x 128 211) or its sums do not fit the workspace (5000
+  // rows 264, all in 256 x 256 387; n 256, k 4096, 8192 rows in 128 x 128 46, 111).
+  if (p.gated) {
+    const int64_t across = ((int64_t)p.n + 127) / 128, fill = across < kCus ? kCus / across * 256 : 256;
+    const int64_t rest = p.m % fill, whole = rest * 4 > fill * 3 || rest * rows_w * 4 > kWorkspace ? p.m : p.m - rest;
+    if (whole > 0) {
+      const DenseParams q = rows_from(p, 0, (int)whole);
+      const hipError_t e = p.out_type == kOutFp8 ? launch<4, 2, 4, 8, 2, kGatedFp8>(q, stream)
+                                                 : launch<4, 2, 4, 8, 2, kGated>(q, stream);
+      if (e != hipSuccess || whole == p.m) return e;
+      return launch_dense(rows_from(p, (uint64_t)whole, (int)rest), stream);
+    }
+  }
   // 128 x 128, two workgroups a CU: 777 rows 62 in two runs (71 in one, 128 x
   // 256 68 to 107) | 36 (128 x 256 42, 64 x 64 and less 62); 8192 rows | 239
   // (256 x 256 250)
-  if (bytes <= kWorkspace && p.m <= kTokens128) {
-    const int64_t s = runs(tiles(128, 128), 512, 1);
-    if (p.gated || kb - kb / s >= kWorthSplit) return launch_split<2, 2, 4, 4, 2>(p, (int)s, stream);
-  }
-  if (!p.gated) return launch<2, 2, 4, 4, 2, kPlain>(p, stream);
-  // 256 x 256: 8192 rows 412 (128 x 256 480), to bf16 400 (128 x 128 422)
-  return p.out_type == kOutFp8 ? launch<4, 2, 4, 8, 2, kGatedFp8>(p, stream)
-                               : launch<4, 2, 4, 8, 2, kGated>(p, stream);
+  const int64_t s = runs(tiles(128, 128), 512, 1);
+  if (p.gated || (p.m <= kTokens128 && kb - kb / s >= kWorthSplit))
+    return launch_split<2, 2, 4, 4, 2>(p, (int)s, stream);
+  return launch<2, 2, 4, 4, 2, kPlain>(p, stream);
 }
 
 }  // namespace llmoe

@@ -453,8 +453,8 @@ int ll_moe_rms_norm(int num_tokens, int hidden, int x_dtype, int out_dtype, floa
  * beside its routed experts. The router gives the dispatch its topk_idx and
  * the combine its topk_weights; a shared expert (or a dense layer) is two
  * products whose result joins the combine's. As above, no page defines these,
- * calls enqueue one or two kernels, may be captured, and the same call gives
- * the same bits.
+ * calls enqueue a few kernels, may be captured, and the same call gives the
+ * same bits.
  */
 
 /*
@@ -548,7 +548,7 @@ int ll_moe_route(int num_tokens, int num_experts, int topk, int logits_dtype, in
  *   LL_MOE_GEMM_MAX_COLUMNS. Apart from the addend, outputs and the workspace
  *   may overlap neither an input nor each other. A row's products are of that
  *   row and the weights alone; how its sum is grouped goes by the sizes of the
- *   call. Enqueued on `stream`.
+ *   call and the row's place in it. Enqueued on `stream`.
  */
 #define LL_MOE_DENSE_WORKSPACE (64 << 20)
 int ll_moe_dense_gemm(int num_tokens, int n, int k, int act, int out_dtype, const void* a,

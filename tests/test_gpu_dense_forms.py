@@ -27,7 +27,8 @@ def test_plain(m, n, k, out, addend):
 @pytest.mark.parametrize("m,n,k", [
     (1, 4112, 1792, ), (7, 4208, 128), (16, 4128, 2048), (17, 2064, 256), (40, 1392, 1920), (64, 2192, 128),
     (100, 592, 3584), (129, 2064, 256), (300, 464, 7168), (700, 1040, 896), (2000, 272, 2048), (4100, 80, 384),
-    (5000, 400, 256), (4097, 2064, 128), (200, 1040, 640)])
+    (5000, 400, 256), (4097, 2064, 128), (200, 1040, 640),
+    (3500, 2064, 256), (15001, 400, 128), (7500, 2064, 128), (300, 32912, 128)])
 def test_gated_to_bf16(m, n, k):
     verify(m, n, k, True, BF16)
 
@@ -35,7 +36,7 @@ def test_gated_to_bf16(m, n, k):
 @pytest.mark.parametrize("m,n,k", [
     (1, 2176, 1792), (9, 4096, 128), (16, 2304, 2048), (17, 1152, 256), (40, 1024, 1920), (64, 2176, 128), (100, 384, 3584),
     (129, 2048, 256), (300, 256, 7168), (700, 1024, 896), (2000, 256, 2048), (4100, 128, 384), (5000, 384, 256),
-    (4097, 2176, 128)])
+    (4097, 2176, 128), (3601, 2176, 128), (4000, 2176, 256), (12000, 512, 128), (300, 32896, 128)])
 def test_gated_to_fp8(m, n, k):
     verify(m, n, k, True, F8)
 
@@ -62,7 +63,7 @@ def test_the_widest_weights_stay_inside_the_workspace(m, n, k, out):
 
 @pytest.mark.parametrize("m,n,k,gated,out", [
     (5, 8208, 256, False, BF16), (40, 1392, 1920, True, BF16), (130, 1040, 7168, False, F32), (700, 1040, 896, True, BF16),
-    (3000, 272, 1024, False, F32), (4100, 384, 256, True, F8), (100, 384, 3584, True, F8), (16, 256, 512, True, F8)])
+    (3000, 272, 1024, False, F32), (4100, 384, 256, True, F8), (100, 384, 3584, True, F8), (16, 256, 512, True, F8), (3500, 2176, 128, True, F8), (4000, 2064, 128, True, BF16)])
 def test_nothing_behind_the_operands_is_read(m, n, k, gated, out):
     """The operands inside larger buffers of NaN, the workspace too."""
     t = make(m, n, k, gated, 3)
