@@ -18,7 +18,7 @@
 // (launch_dense says which sizes take which).
 //
 // Bound: few rows are latency and a second launch (one row, gated, n 2048, k
-// 7168, 29 MB: 8.4 us to bf16, 10.9 to fp8, of which 2.0 are the second
+// 7168, 29 MB: 8.3 us to bf16, 10.8 to fp8, of which 2.0 are the second
 // kernel and the rest its launch). Many rows: 8192 x 4096 x 7168 take 400 us, 1.2 PFLOP/s; the copies
 // alone take 203 of them and the products without copies 340, which overlap no
 // better: a SIMD's matrix unit is busy 52 % of the time, and 2.8 vector
@@ -37,17 +37,15 @@ namespace {
 enum : int { kPartial = 0, kPlain = 1, kGated = 2, kGatedFp8 = 3 };
 static_assert(kStep == kFp8Block);  // a k step is one scale's columns
 constexpr int64_t kWorkspace = LL_MOE_DENSE_WORKSPACE;
-// Up to so many workgroups there are 16 x 16 tiles, and up to so many tiles 64 x
-// 64 ones, with more or fewer steps of k than kDeep; rows up to which a tile has
-// 16, 64 and 128 of them all the same; steps of k that a split has to save, to be
-// worth its second kernel (17 rows, n 1040, k 4096: 10.4 us, in four runs 8.0; 1
-// row, n 7168, k 2048: 7.2, in two 8.2).
-constexpr int kFew = 512, kFewToFp8 = 256;
-constexpr int kDeep = 40, kTiles64 = 512, kTiles64Deep = 256;
-constexpr int kDeepGated = 24, kTiles64Gated = 256, kTiles64GatedDeep = 128;
+// Few steps of k; CUs; up to so many tiles there are 64 x 64 ones, with many
+// steps and with few; rows up to which a tile has 16, 64 and 128 of them all the
+// same; steps of k that a split has to save, to be worth its second kernel (1 row,
+// n 7168, k 2048: 7.2 us, in two runs 8.2).
+constexpr int kShort = 40, kShortGated = 24;
+constexpr int64_t kCus = 256;
+constexpr int kTiles64 = 512, kTiles64Deep = 256, kTiles64Gated = 256, kTiles64GatedDeep = 128;
 constexpr int kTokens16 = 32, kTokens16Gated = 16, kTokens64 = 64, kTokens128 = 4096;
 constexpr int kWorthSplit = 12;
-constexpr int64_t kCus = 256;
 
 // WM x WN wavefronts, each FM x FN fragments of 16 x 16; STAGES buffers of a
 // step in LDS. The steps of k are divided among `splits` workgroups.
@@ -258,95 +256,107 @@ __global__ void __launch_bounds__(WM* WN * 64, 2) dense_kernel(const DenseParams
   }
 }
 
-// A few rows: 16 rows of A by 16 of W, whose columns the wavefronts split and
-// whose sums meet in LDS, so that one launch does it. Gated, the 16 are 8 gate
-// rows and the 8 up rows of the same columns; their values go out in bf16, or
-// (kValues) in fp32 to the workspace, for dense_finish_kernel to quantize.
-// Rows come by whole lines into registers, D steps ahead, and through LDS
-// into the products' order.
+// A few rows: 16 or 32 rows of A by 16 of W, whose columns the wavefronts split
+// and whose sums meet in LDS, so that one launch does it. Gated, the 16 are 8
+// gate rows and the 8 up rows of the same columns; their values go out in bf16,
+// or (kValues) in fp32 to the workspace, for dense_finish_kernel to quantize.
+// Rows come by whole lines into registers, a step ahead, and through LDS into
+// the products' order. Eight wavefronts, so that a CU has up to four workgroups
+// under way (one row, gated to bf16, n 2048, k 7168: 8.3 us, with sixteen 9.1;
+// two steps ahead 8.4).
 enum : int { kValues = 4 };
-template <int WAVES, int D, int MODE>
-__global__ void __launch_bounds__(WAVES * 64) dense_few_kernel(const DenseParams P) {
+template <int FM, int MODE>
+__global__ void __launch_bounds__(512) dense_few_kernel(const DenseParams P) {
   constexpr bool GATED = MODE != kPlain;
-  constexpr int COLS = GATED ? 8 : 16, PART = 16 * kStep;
-  __shared__ __align__(16) uint8_t pool[WAVES * 2 * PART];
+  constexpr int WAVES = 8;
+  constexpr int ROWS = 16 * FM, COLS = GATED ? 8 : 16, PART = 16 * kStep;
+  __shared__ __align__(16) uint8_t pool[WAVES * (FM + 1) * PART];
   const int lane = threadIdx.x & 63, lo = lane & 15, hi = lane >> 4;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const uint32_t ld = (uint32_t)P.k;
   const int kb = P.k / 128;
   const int s0 = kb * wave / WAVES, s1 = kb * (wave + 1) / WAVES;
   const uint32_t across = (uint32_t)(P.n / COLS);
-  const int64_t row0 = (int64_t)(blockIdx.x / across) * 16;
+  const int64_t row0 = (int64_t)(blockIdx.x / across) * ROWS;
   const int col0 = (int)(blockIdx.x % across) * COLS;
-  const int rows = P.m - row0 < 16 ? (int)(P.m - row0) : 16;
+  const int rows = P.m - row0 < ROWS ? (int)(P.m - row0) : ROWS;
   const int second = GATED ? P.n + col0 : col0 + 8;  // rows 8-15 of W
   const Rsrc ra = rsrc_of(P.a + (uint64_t)row0 * ld, (uint32_t)rows * ld);
   const Rsrc rw0 = rsrc_of(P.w + (uint64_t)col0 * ld, 8 * ld), rw1 = rsrc_of(P.w + (uint64_t)second * ld, 8 * ld);
   const Rsrc ras = rsrc_of(P.a_scales + (uint64_t)row0 * kb, (uint32_t)rows * kb * 4u);
   const Rsrc rws = rsrc_of(P.w_scales, (uint32_t)((GATED ? 2 * P.n : P.n) + 127) / 128 * kb * 4u);
   const uint32_t my_block = 4u * (uint32_t)((hi < 2 ? col0 : second) / 128 * kb);
-  uint8_t* al = pool + wave * 2 * PART;
+  uint8_t* al = pool + wave * (FM + 1) * PART;  // rows of W, then of A
   uint32_t apart = 0;
   asm volatile("" : "+v"(apart));  // lanes read each other's rows: no read moves across the writes
   const uint8_t* ar = al + apart;
   const uint32_t r8 = (uint32_t)lane >> 3, mine = r8 * ld + (lane & 7) * 16;
 
-  v4u ab[D][2], wb[D][2];
-  float as[D], ws[D];
-  auto load = [&](int s, int step) {
+  v4u ab[2 * FM], wb[2];
+  float as[FM], ws;
+  auto load = [&](int step) {
     const uint32_t at = step < s1 ? (uint32_t)step * kStep : kOutside, sc = step < s1 ? 4u * (uint32_t)step : kOutside;
-    wb[s][0] = __builtin_amdgcn_raw_buffer_load_b128(rw0, (int)(mine + at), 0, 0);
-    wb[s][1] = __builtin_amdgcn_raw_buffer_load_b128(rw1, (int)(mine + at), 0, 0);
-    ab[s][0] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(mine + at), 0, 0);
-    ab[s][1] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(mine + 8 * ld + at), 0, 0);
-    as[s] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(ras, (int)(4u * (uint32_t)(lo * kb) + sc), 0, 0));
-    ws[s] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, (int)(my_block + sc), 0, 0));
+    wb[0] = __builtin_amdgcn_raw_buffer_load_b128(rw0, (int)(mine + at), 0, 0);
+    wb[1] = __builtin_amdgcn_raw_buffer_load_b128(rw1, (int)(mine + at), 0, 0);
+#pragma unroll
+    for (int i = 0; i < 2 * FM; ++i)
+      ab[i] = __builtin_amdgcn_raw_buffer_load_b128(ra, (int)(mine + 8 * i * ld + at), 0, 0);
+#pragma unroll
+    for (int m = 0; m < FM; ++m)
+      as[m] = __uint_as_float(
+          __builtin_amdgcn_raw_buffer_load_b32(ras, (int)(4u * (uint32_t)((16 * m + lo) * kb) + sc), 0, 0));
+    ws = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(rws, (int)(my_block + sc), 0, 0));
   };
-  auto store = [&](int s) {
+  auto store = [&] {
     const uint32_t at = r8 * kStep + (((lane & 7) ^ r8) & 7) * 16;
-    *reinterpret_cast<v4u*>(al + at) = ab[s][0];
-    *reinterpret_cast<v4u*>(al + 8 * kStep + at) = ab[s][1];
-    *reinterpret_cast<v4u*>(al + PART + at) = wb[s][0];
-    *reinterpret_cast<v4u*>(al + PART + 8 * kStep + at) = wb[s][1];
+    *reinterpret_cast<v4u*>(al + at) = wb[0];
+    *reinterpret_cast<v4u*>(al + 8 * kStep + at) = wb[1];
+#pragma unroll
+    for (int i = 0; i < 2 * FM; ++i) *reinterpret_cast<v4u*>(al + PART + 8 * i * kStep + at) = ab[i];
   };
   auto chunk = [&](int part, int c) {
     return fp8_to_bf16(*reinterpret_cast<const v4u*>(ar + part + lo * kStep + ((c ^ lo) & 7) * 16));
   };
-  f32x4 acc = {0, 0, 0, 0};
+  f32x4 acc[FM];
 #pragma unroll
-  for (int s = 0; s < D; ++s) load(s, s0 + s);
-  for (int k = s0; k < s1; k += D) {
+  for (int m = 0; m < FM; ++m) acc[m] = f32x4{0, 0, 0, 0};
+  load(s0);
+  for (int k = s0; k < s1; ++k) {
+    store();
+    float sc[FM];
 #pragma unroll
-    for (int s = 0; s < D; ++s) {
-      if (k + s < s1) {
-        store(s);
-        const float sc = as[s] * ws[s];
-        load(s, k + s + D);
-        f32x4 p = {0, 0, 0, 0};
+    for (int m = 0; m < FM; ++m) sc[m] = as[m] * ws;
+    load(k + 1);
+    const Bf16x16 w[2] = {chunk(0, hi), chunk(0, 4 + hi)};
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
-          const Bf16x16 a = chunk(0, 4 * j + hi), w = chunk(PART, 4 * j + hi);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.lo, a.lo, p, 0, 0, 0);
-          p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w.hi, a.hi, p, 0, 0, 0);
-        }
+    for (int m = 0; m < FM; ++m) {
+      f32x4 p = {0, 0, 0, 0};
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[r] = __builtin_fmaf(sc, p[r], acc[r]);
+      for (int j = 0; j < 2; ++j) {
+        const Bf16x16 a = chunk((m + 1) * PART, 4 * j + hi);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j].lo, a.lo, p, 0, 0, 0);
+        p = __builtin_amdgcn_mfma_f32_16x16x32_bf16(w[j].hi, a.hi, p, 0, 0, 0);
       }
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[m][r] = __builtin_fmaf(sc[m], p[r], acc[m][r]);
     }
   }
   // the wavefronts' sums meet: lane l holds W rows 4 (l / 16) + r of row l % 16
   __syncthreads();
   float* sums = reinterpret_cast<float*>(pool);
-  *reinterpret_cast<f32x4*>(sums + wave * 256 + lo * 16 + 4 * hi) = acc;
+#pragma unroll
+  for (int m = 0; m < FM; ++m)
+    *reinterpret_cast<f32x4*>(sums + wave * (ROWS * 16) + (16 * m + lo) * 16 + 4 * hi) = acc[m];
   __syncthreads();
   const int t = threadIdx.x;
-  if (t < 16 * COLS) {
+  static_assert(ROWS * COLS <= WAVES * 64);
+  if (t < ROWS * COLS) {
     const int r = t / COLS, c = t % COLS;
     float v = 0.0f, u = 0.0f;
 #pragma unroll
     for (int w = 0; w < WAVES; ++w) {
-      v += sums[w * 256 + r * 16 + c];
-      if (GATED) u += sums[w * 256 + r * 16 + 8 + c];
+      v += sums[w * (ROWS * 16) + r * 16 + c];
+      if (GATED) u += sums[w * (ROWS * 16) + r * 16 + 8 + c];
     }
     if (GATED) v = silu_mul(v, u);
     if (r < rows) {
@@ -405,12 +415,12 @@ hipError_t launch_finish(const DenseParams& p, int splits, hipStream_t stream) {
   return hipGetLastError();
 }
 
-template <int WAVES, int D>
+template <int FM>
 hipError_t launch_few(const DenseParams& p, hipStream_t stream) {
-  const unsigned blocks = (unsigned)((p.m + 15) / 16 * (p.n / (p.gated ? 8 : 16)));
-  if (!p.gated) dense_few_kernel<WAVES, D, kPlain><<<blocks, WAVES * 64, 0, stream>>>(p);
-  else if (p.out_type == kOutFp8) dense_few_kernel<WAVES, D, kValues><<<blocks, WAVES * 64, 0, stream>>>(p);
-  else dense_few_kernel<WAVES, D, kGated><<<blocks, WAVES * 64, 0, stream>>>(p);
+  const unsigned blocks = (unsigned)(((int64_t)p.m + 16 * FM - 1) / (16 * FM) * (p.n / (p.gated ? 8 : 16)));
+  if (!p.gated) dense_few_kernel<FM, kPlain><<<blocks, 512, 0, stream>>>(p);
+  else if (p.out_type == kOutFp8) dense_few_kernel<FM, kValues><<<blocks, 512, 0, stream>>>(p);
+  else dense_few_kernel<FM, kGated><<<blocks, 512, 0, stream>>>(p);
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || p.out_type != kOutFp8) return e;
   DenseParams q = p;
@@ -478,15 +488,22 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
     if (s > kWorkspace / bytes) s = kWorkspace / bytes;
     return s < 1 ? 1 : s;
   };
-  // 16 x 16 while those are few: to bf16 1 row 8.4 (16 x 64 tiles in four runs
-  // of k 11.7), 32 rows 13.8 (16.0), 48 rows 17.9 (15.6 in 64 x 64); | 1 row 6.0
-  // (7.0), 32 rows 10.0 (7.7); 512 rows, n 256, k 2048, to bf16 5.8 (64 x 64
-  // 9.1). To fp8 the second kernel is needed all the same: 1 row 10.9 (12.0),
-  // with n and k 4096 11.9 (11.1).
-  const int64_t few = ((int64_t)p.m + 15) / 16 * (p.n / (p.gated ? 8 : 16));
-  if (few <= (p.out_type == kOutFp8 ? kFewToFp8 : kFew)) return launch_few<16, 1>(p, stream);
-  // 16 x 64: n and k 4096, gated, 1 row 11.1 in two runs (14.4 in one, 64 x 64
-  // 13.9); | 32 rows 7.7 (64 x 64 10.9)
+  // 16 x 16 or 32 x 16 while those are few. To bf16, n 2048: 1 row 8.3 (16 x 64
+  // tiles in two runs of k 13.5), 17 rows in 32 x 16 10.1 (16 x 16 12.3, 64 x 64
+  // 14.7), 32 rows 12.8 (14.1, 15.1); 64 rows of n 1536, k 2048 in 16 x 16 6.5
+  // (9.7), k 7168 16.8 (16.4); 16 rows of n 2560, k 7168 16.3 (15.0). | 1 row 5.4 (7.0), 16 rows 6.2 (7.4). To fp8 the
+  // second kernel is needed all the same: 1 row 10.8 (12.0 in four), n and k 4096
+  // 11.4 (11.0), 16 rows 13.4 (11.9), n 4096 and k 1024 6.5 (7.5). 64 rows of n 3584, k
+  // 2048, plain in 32 x 16 7.0 (9.7), k 7168 19.0 (16.4).
+  const bool fp8 = p.out_type == kOutFp8, few_steps = kb <= (fp8 ? kShortGated : kShort);
+  const int64_t strips = p.n / (p.gated ? 8 : 16);
+  const int64_t of16 = ((int64_t)p.m + 15) / 16 * strips, of32 = ((int64_t)p.m + 31) / 32 * strips;
+  if (p.m > 16 && of16 > kCus && of32 <= kCus) return launch_few<2>(p, stream);
+  const bool less = p.gated && !few_steps && (fp8 || (p.m > 8 && p.m <= 16));
+  if (of16 <= (less ? kCus : 3 * kCus)) return launch_few<1>(p, stream);
+  if (p.m > 16 && of32 <= 2 * kCus && few_steps) return launch_few<2>(p, stream);
+  // 16 x 64: 16 rows, gated, n 4096, k 7168 16.1 in two runs (16 x 16 19.1, 64 x
+  // 64 20.0); plain, n 16384, k 2048 8.5 (11.1, 10.6)
   if (p.gated && p.m <= kTokens16Gated && bytes <= kWorkspace)
     return launch_split<1, 4, 1, 1, 4>(p, (int)runs(tiles(16, 64), 256, 2), stream);
   if (!p.gated && p.m <= kTokens16) return launch<1, 4, 1, 1, 4, kPlain>(p, stream);
@@ -496,8 +513,8 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   // (29.5); 1024 rows, k 2048 17.3 (21.4), k 7168 50.4 (43.8). Gated, n 1024: 256
   // rows, k 1024 9.5 (13.2), k 7168 21.5 (26.3); 512 rows, k 1024 11.3 (15.4), k
   // 7168 31.8 (30.0)
-  const int64_t most64 = p.gated ? (kb > kDeepGated ? kTiles64GatedDeep : kTiles64Gated)
-                                 : (kb > kDeep ? kTiles64Deep : kTiles64);
+  const int64_t most64 = p.gated ? (kb > kShortGated ? kTiles64GatedDeep : kTiles64Gated)
+                                 : (few_steps ? kTiles64 : kTiles64Deep);
   if (p.m <= kTokens64 || tiles(64, 64) <= most64) {
     const int64_t s = runs(tiles(64, 64), 256, 1);
     if ((p.gated && bytes <= kWorkspace) || kb - kb / s >= kWorthSplit)
