@@ -491,10 +491,11 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   // 16 x 16 or 32 x 16 while those are few. To bf16, n 2048: 1 row 8.3 (16 x 64
   // tiles in two runs of k 13.5), 17 rows in 32 x 16 10.1 (16 x 16 12.3, 64 x 64
   // 14.7), 32 rows 12.8 (14.1, 15.1); 64 rows of n 1536, k 2048 in 16 x 16 6.5
-  // (9.7), k 7168 16.8 (16.4); 16 rows of n 2560, k 7168 16.3 (15.0). | 1 row 5.4 (7.0), 16 rows 6.2 (7.4). To fp8 the
-  // second kernel is needed all the same: 1 row 10.8 (12.0 in four), n and k 4096
-  // 11.4 (11.0), 16 rows 13.4 (11.9), n 4096 and k 1024 6.5 (7.5). 64 rows of n 3584, k
-  // 2048, plain in 32 x 16 7.0 (9.7), k 7168 19.0 (16.4).
+  // (9.7), k 7168 16.8 (16.4); 16 rows of n 2560, k 7168 16.3 (15.0). | 1 row 5.4
+  // (7.0), 16 rows 6.2 (7.4). To fp8 the second kernel is needed all the same: 1
+  // row 10.8 (12.0 in four), n and k 4096 11.4 (11.0), 16 rows 13.4 (11.9), n 4096
+  // and k 1024 6.5 (7.5). 64 rows of n 3584, k 2048, plain in 32 x 16 7.0 (9.7), k
+  // 7168 19.0 (16.4).
   const bool fp8 = p.out_type == kOutFp8, few_steps = kb <= (fp8 ? kShortGated : kShort);
   const int64_t strips = p.n / (p.gated ? 8 : 16);
   const int64_t of16 = ((int64_t)p.m + 15) / 16 * strips, of32 = ((int64_t)p.m + 31) / 32 * strips;
