@@ -128,8 +128,9 @@ __global__ void __launch_bounds__(64) gate_row_kernel(const GateParams P) {
 
 // 16 tokens x EW experts (as few as the GPU has room for). fp32 weights are
 // cut on their way into LDS, once each (cut as fragments, whose 16 rows repeat
-// the EW, 128 tokens by 256 experts took 11.2 us).
-template <bool FP32, int EW, int WAVES, int D>
+// the EW, 128 tokens by 256 experts took 11.2 us, as it is 10.7, and with loads
+// one step ahead instead of two 9.2: fewer registers, more wavefronts).
+template <bool FP32, int EW, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P) {
   constexpr int ITEM = FP32 ? 4 : 2, WROW = kColumns * ITEM, WL = (EW * WROW + 1023) / 1024;
   constexpr int XPART = 16 * 128, PARTS = FP32 ? 3 : 1, WPART = PARTS * EW * 128;
@@ -153,29 +154,29 @@ __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P
     const int experts = P.num_experts - e0 < EW ? P.num_experts - e0 : EW;
     const Rsrc rx = rsrc_of(P.x + (uint64_t)row0 * ldx, (uint32_t)rows * ldx);
     const Rsrc rw = rsrc_of(P.w + (uint64_t)e0 * ldw, (uint32_t)experts * ldw);
-    v4u xb[D][2], wb[D][WL];
-    auto load = [&](int s, int step) {
+    v4u xb[2], wb[WL];
+    auto load = [&](int step) {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const uint32_t at = (uint32_t)step * 128 + (lane & 7) * 16;
-        xb[s][i] = __builtin_amdgcn_raw_buffer_load_b128(
+        xb[i] = __builtin_amdgcn_raw_buffer_load_b128(
             rx, (int)(step < s1 && at < ldx ? ((lane >> 3) + 8 * i) * ldx + at : kOutside), 0, 0);
       }
 #pragma unroll
       for (int i = 0; i < WL; ++i) {
         constexpr int CH = WROW / 16;
         const uint32_t at = (uint32_t)step * WROW + (lane % CH) * 16;
-        wb[s][i] = __builtin_amdgcn_raw_buffer_load_b128(
+        wb[i] = __builtin_amdgcn_raw_buffer_load_b128(
             rw, (int)(step < s1 && at < ldw && lane / CH + 64 / CH * i < EW ? (lane / CH + 64 / CH * i) * ldw + at
                                                                              : kOutside),
             0, 0);
       }
     };
-    auto store = [&](int s) {
+    auto store = [&] {
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
         const int r = (lane >> 3) + 8 * i;
-        *reinterpret_cast<v4u*>(xl + r * 128 + (((lane & 7) ^ r) & 7) * 16) = xb[s][i];
+        *reinterpret_cast<v4u*>(xl + r * 128 + (((lane & 7) ^ r) & 7) * 16) = xb[i];
       }
 #pragma unroll
       for (int i = 0; i < WL; ++i) {
@@ -183,12 +184,12 @@ __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P
         const int r = lane / CH + 64 / CH * i, c = lane % CH;
         if (64 / CH > EW && r >= EW) continue;
         if constexpr (FP32) {
-          const Parts4 v = cut(wb[s][i]);
+          const Parts4 v = cut(wb[i]);
 #pragma unroll
           for (int p = 0; p < 3; ++p)
             *reinterpret_cast<v2u*>(wl + (p * EW + r) * 128 + ((c / 2 ^ r) & 7) * 16 + (c & 1) * 8) = v.part[p];
         } else {
-          *reinterpret_cast<v4u*>(wl + r * 128 + ((c ^ r) & 7) * 16) = wb[s][i];
+          *reinterpret_cast<v4u*>(wl + r * 128 + ((c ^ r) & 7) * 16) = wb[i];
         }
       }
     };
@@ -206,17 +207,11 @@ __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(chunk(wr + p * EW * 128, wrow, 4 * j + hi), a, acc, 0, 0, 0);
       }
     };
-#pragma unroll
-    for (int s = 0; s < D; ++s) load(s, s0 + s);
-    for (int k = s0; k < s1; k += D) {
-#pragma unroll
-      for (int s = 0; s < D; ++s) {
-        if (k + s < s1) {
-          store(s);
-          load(s, k + s + D);
-          multiply();
-        }
-      }
+    load(s0);
+    for (int k = s0; k < s1; ++k) {
+      store();
+      load(k + 1);
+      multiply();
     }
     // the wavefronts' sums meet: lane l holds experts 4 (l / 16) + r of token l % 16
     __syncthreads();
@@ -372,11 +367,11 @@ hipError_t launch_tile(const GateParams& p, hipStream_t stream) {
   return hipSuccess;
 }
 
-template <bool FP32, int EW, int WAVES, int D>
+template <bool FP32, int EW, int WAVES>
 hipError_t launch_few(const GateParams& p, hipStream_t stream) {
   const int64_t tiles = (((int64_t)p.num_tokens + 15) / 16) * ((p.num_experts + EW - 1) / EW);
   const unsigned blocks = (unsigned)(tiles < 1 << 16 ? tiles : 1 << 16);
-  gate_few_kernel<FP32, EW, WAVES, D><<<blocks, WAVES * 64, 0, stream>>>(p);
+  gate_few_kernel<FP32, EW, WAVES><<<blocks, WAVES * 64, 0, stream>>>(p);
   return hipGetLastError();
 }
 
@@ -393,10 +388,11 @@ hipError_t launch_row(const GateParams& p, hipStream_t stream) {
 // Which kernel, by the sizes (us at hidden 7168 and 256 experts, weights bf16 |
 // fp32). Up to kRowTokens tokens: a wavefront an expert (1 token 3.5 | 4.2, where
 // 16 x 8 take 6.0 | 9.6; 4 tokens 6.1 | 6.5 against 6.0 | 9.8). Then 16 tokens
-// by as few experts as fill the GPU once (64 tokens: 16 x 4 6.8 | 8.6, 16 x 8 6.8 |
-// 10.0, 16 x 16 8.3 | 12.7; 128 tokens 16 x 8 7.2 | 10.5; 256 tokens 16 x 16 9.1 |
-// 13.7), up to as many logits as tiles do faster (768 tokens 19.2 against 21.3,
-// 1024 tokens 31 against 24 | 46 against 48). Then the smallest tiles that are
+// by as few experts as fill the GPU once (64 tokens: 16 x 4 6.3 | 8.2, 16 x 8 6.4 |
+// 8.9, 16 x 16 7.7 | 11.2; 128 tokens 10.4 | 13.5, 6.7 | 9.2, 7.9 | 11.4; 256 tokens
+// 16 x 16 8.4 | 12.1), more than 256 of those with eight wavefronts (512 tokens 13.2 |
+// 21.6, with sixteen 13.7 | 22.4), up to as many logits as tiles do faster (768
+// tokens 18.7 against 21.3, 1024 tokens 27 against 24 | 44 against 48). Then the smallest tiles that are
 // not too many: 64 x 32 (2048 tokens 30 | 51, in 64 x 64 34 | 79; 4096 tokens 50 |
 // 77), then with bf16 64 x 64 (4096 tokens 36; 8192 63), 64 x 128, two a CU (4096
 // tokens 52, 8192 54, 10000 96), and 128 x 128 (8192 tokens 70, 10000 71, 16384
@@ -411,17 +407,17 @@ hipError_t launch_gate(const GateParams& p, hipStream_t stream) {
   const int64_t logits = (int64_t)p.num_tokens * p.num_experts;
   if (p.w_fp32) {
     if (logits <= kFewLogitsFp32) {
-      if (tiles(16, 4) <= kCus) return launch_few<true, 4, 16, 2>(p, stream);
-      if (tiles(16, 8) <= kCus) return launch_few<true, 8, 16, 2>(p, stream);
-      return tiles(16, 16) <= kCus ? launch_few<true, 16, 16, 2>(p, stream) : launch_few<true, 16, 8, 2>(p, stream);
+      if (tiles(16, 4) <= kCus) return launch_few<true, 4, 16>(p, stream);
+      if (tiles(16, 8) <= kCus) return launch_few<true, 8, 16>(p, stream);
+      return tiles(16, 16) <= kCus ? launch_few<true, 16, 16>(p, stream) : launch_few<true, 16, 8>(p, stream);
     }
     if (tiles(64, 32) <= 2 * kCus) return launch_tile<true, 2, 2, 2, 1, 4>(p, stream);
     return tiles(128, 64) < 2 * kCus ? launch_tile<true, 2, 2, 4, 1, 2>(p, stream)
                                      : launch_tile<true, 2, 2, 4, 2, 2>(p, stream);
   }
   if (logits <= kFewLogits) {
-    if (tiles(16, 8) <= kCus) return launch_few<false, 8, 16, 2>(p, stream);
-    return tiles(16, 16) <= kCus ? launch_few<false, 16, 16, 2>(p, stream) : launch_few<false, 16, 8, 2>(p, stream);
+    if (tiles(16, 8) <= kCus) return launch_few<false, 8, 16>(p, stream);
+    return tiles(16, 16) <= kCus ? launch_few<false, 16, 16>(p, stream) : launch_few<false, 16, 8>(p, stream);
   }
   if (tiles(64, 32) <= kCus) return launch_tile<false, 2, 2, 2, 1, 4>(p, stream);
   if (tiles(64, 64) <= kCus) return launch_tile<false, 2, 2, 2, 2, 4>(p, stream);
