@@ -541,6 +541,15 @@ hipError_t launch_dense(const DenseParams& p, hipStream_t stream) {
   // 128 x 128, two workgroups a CU: 777 rows 62 in two runs (71 in one, 128 x
   // 256 68 to 107) | 36 (128 x 256 42, 64 x 64 and less 62); 8192 rows | 239
   // (256 x 256 250)
+  // Gated and deep, rows little beyond 256 or 512 of those tiles go out in two
+  // parts, too (1100 rows 90, together 105; 2200 rows 143, 160).
+  if (p.gated && kb > kShortGated) {
+    const int64_t fill = kCus / ((rows_w + 127) / 128) * 128, rest = fill ? p.m % fill : 0, times = fill ? p.m / fill : 0;
+    if (rest > 0 && ((times == 1 && rest * 4 <= fill) || (times == 2 && rest * 2 <= fill))) {
+      const hipError_t e = launch_dense(rows_from(p, 0, (int)(p.m - rest)), stream);
+      return e != hipSuccess ? e : launch_dense(rows_from(p, (uint64_t)(p.m - rest), (int)rest), stream);
+    }
+  }
   const int64_t s = runs(tiles(128, 128), 512, 1);
   if (p.gated || (p.m <= kTokens128 && kb - kb / s >= kWorthSplit))
     return launch_split<2, 2, 4, 4, 2>(p, (int)s, stream);

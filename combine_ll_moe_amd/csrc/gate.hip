@@ -13,9 +13,9 @@
 // split among the wavefronts (gate_few_kernel); tiles that come straight into
 // LDS, steps ahead of the products (gate_tile_kernel).
 //
-// Bound: one token 3.5 us with bf16 weights (3.7 MB) and a decode batch 7 are
-// latency: a launch, loads, and the sums' meeting. 16384 tokens (hidden 7168,
-// 256 experts, bf16) take 79 us, 760 TFLOP/s; their operands pass from the
+// Bound: one token 3.5 us with bf16 weights (3.7 MB) and 128 tokens 6.7
+// are latency: a launch, loads, and the sums' meeting. 16384 tokens (hidden 7168,
+// 256 experts, bf16) take 78 to 80 us, 750 to 770 TFLOP/s; their operands pass from the
 // caches to LDS at 12 TB/s, and each SIMD's one or two wavefronts wait for each
 // other at every step.
 #include <hip/hip_runtime.h>

@@ -32,7 +32,8 @@ def test_plain(m, n, k, out, addend):
     (100, 592, 3584), (129, 2064, 256), (300, 464, 7168), (700, 1040, 896), (2000, 272, 2048), (4100, 80, 384),
     (5000, 400, 256), (4097, 2064, 128), (200, 1040, 640),
     (3, 6160, 640), (16, 8208, 128), (11, 2576, 5376), (20, 1616, 896), (31, 2064, 256), (64, 1808, 384), (40, 2064, 1920),
-    (64, 4112, 384), (3500, 2064, 256), (15001, 400, 128), (7500, 2064, 128), (300, 32912, 128)])
+    (64, 4112, 384), (3500, 2064, 256), (15001, 400, 128), (7500, 2064, 128), (300, 32912, 128), (950, 2064, 3200),
+    (1900, 2064, 3328)])
 def test_gated_to_bf16(m, n, k):
     verify(m, n, k, True, BF16)
 
@@ -41,7 +42,7 @@ def test_gated_to_bf16(m, n, k):
     (1, 2176, 1792), (9, 4096, 128), (16, 2304, 2048), (17, 1152, 256), (40, 1024, 1920), (64, 2176, 128), (100, 384, 3584),
     (129, 2048, 256), (300, 256, 7168), (700, 1024, 896), (2000, 256, 2048), (4100, 128, 384), (5000, 384, 256),
     (4097, 2176, 128), (3, 6272, 512), (16, 2304, 3328), (20, 1664, 896), (40, 2176, 1920), (60, 1664, 512), (64, 896, 256),
-    (3601, 2176, 128), (4000, 2176, 256), (12000, 512, 128), (300, 32896, 128)])
+    (3601, 2176, 128), (4000, 2176, 256), (12000, 512, 128), (300, 32896, 128), (1100, 2048, 3200), (2300, 2048, 3328)])
 def test_gated_to_fp8(m, n, k):
     verify(m, n, k, True, F8)
 
