@@ -477,38 +477,31 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
         const float off = 0x1p-19f + 0x1p-20f * size;
         const bool tight = out > none32 && !(in - out > off);
         if (__ballot(tight)) {
-          // The values of the groups again, to 1e-10, from the members that
-          // make them, if fp32 tells which those are: one value each within
-          // `off` of the first and of the second.
+          // The values of the groups again, to 1e-10: the best two (or one) of
+          // every member within `off` of the second (first), among which they
+          // are, however near to each other
+          const float from = (sums ? second : first) - off;
           double top1 = none(), top2 = none();
-          uint32_t n1 = 0, n2 = 0;
+          auto enter64 = [&](double t1, double t2) {
+            top2 = fmax(fmax(top2, t2), fmin(top1, t1));
+            top1 = fmax(top1, t1);
+          };
 #pragma unroll
           for (int i = 0; i < V; ++i) {
             const float x = !SCORED && sums ? (l[i] > none32 ? score32(l[i]) : none32) : key[i];
-            const bool is1 = x > none32 && x >= first - off, is2 = x > none32 && !is1 && x >= second - off;
-            if (is1 || (is2 && sums)) {
-              const double v = score64(l[i]) + (SCORED ? (double)counted(b[i]) : 0.0);
-              if (is1) top1 = v, ++n1;
-              else top2 = v, ++n2;
-            }
+            if (x > none32 && x >= from) enter64(score64(l[i]) + (SCORED ? (double)counted(b[i]) : 0.0), none());
           }
-          auto join64 = [&](double o1, double o2, uint32_t c1, uint32_t c2) {
-            top1 = fmax(top1, o1), top2 = fmax(top2, o2), n1 += c1, n2 += c2;
-          };
-          if (lanes >= 2) join64(dpp<0xB1>(top1), dpp<0xB1>(top2), dpp<0xB1>(n1), dpp<0xB1>(n2));
-          if (lanes >= 4) join64(dpp<0x4E>(top1), dpp<0x4E>(top2), dpp<0x4E>(n1), dpp<0x4E>(n2));
-          if (lanes >= 8) join64(dpp<0x141>(top1), dpp<0x141>(top2), dpp<0x141>(n1), dpp<0x141>(n2));
+          if (lanes >= 2) enter64(dpp<0xB1>(top1), dpp<0xB1>(top2));
+          if (lanes >= 4) enter64(dpp<0x4E>(top1), dpp<0x4E>(top2));
+          if (lanes >= 8) enter64(dpp<0x141>(top1), dpp<0x141>(top2));
           const double exact = sums ? top1 + top2 : top1;
-          const bool told = mine == none32 || (n1 == 1 && (!sums || n2 == 1));
-          // (a value that is not told may be 2 off below what it is)
-          const bool at_border = mine > none32 && !(fabsf(mine - in) > 4 * off && fabsf(mine - out) > 4 * off);
           const bool kept64 = rank((uint64_t)ordered(exact)) < stay;
           const double in64 = -row_max(kept64 ? -exact : none()), out64 = row_max(kept64 ? none() : exact);
           const double off64 = 0x1p-30 + 0x1p-48 * (double)size;
           // (the border of 64 bits must not be a tie either: equal values stay
           // or go together there, and then not as many groups stay as should)
           const uint32_t staying = (uint32_t)__popcll(__ballot(kept64) >> (lane & 48) & 0xFFFF);
-          const bool left = (at_border && !told) || staying != stay || !(in64 - out64 > off64);
+          const bool left = staying != stay || !(in64 - out64 > off64);
           unsure = tight && row_max(left ? 1.0f : 0.0f) > 0.0f;
           kept = tight ? kept64 : kept;
         }
