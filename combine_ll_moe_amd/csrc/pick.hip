@@ -465,7 +465,8 @@ __global__ void __launch_bounds__(kRowsAtOnce * 64) pick_rows_kernel(const PickP
       if (lanes >= 2) join(dpp<0xB1>(first), dpp<0xB1>(second));
       if (lanes >= 4) join(dpp<0x4E>(first), dpp<0x4E>(second));
       if (lanes >= 8) join(dpp<0x141>(first), dpp<0x141>(second));
-      const float mine = sums ? first + second : first;
+      // (a sum below fp32's values is still that of a group that has its two)
+      const float mine = !sums ? first : second > none32 ? fmaxf(first + second, -FLT_MAX) : none32;
       // every lane of a better group stands before this one's
       const uint32_t stay = P.topk_groups * lanes;
       bool kept = rank((uint64_t)ordered(mine) << 32 | (uint32_t)(16 - l16 / lanes)) < stay;

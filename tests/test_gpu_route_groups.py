@@ -157,3 +157,36 @@ def test_rows_of_zeros_with_a_stepped_bias(e, groups, topk_groups, sigmoid):
     for _ in range(300):
         b = (np.round(rng.standard_normal(e) * 30) * 1e-3).astype(np.float32)
         verify_rows(x, 8, sigmoid, torch.from_numpy(b).to(DEV), groups, topk_groups)
+
+
+@pytest.mark.parametrize("e,groups,topk_groups", SHAPES)
+@pytest.mark.parametrize("sigmoid", [True, False])
+def test_sums_of_two_beyond_fp32(e, groups, topk_groups, sigmoid):
+    """Biases that mask by the type's lowest value and others as large: a
+    group's sum of two leaves fp32, but it stands before a group that has fewer
+    than two experts left, and in its place among the others."""
+    say("sums beyond fp32", e, groups, topk_groups, sigmoid)
+    rng = np.random.default_rng(e + groups)
+    per = e // groups
+    for draw in range(24):
+        x = rng.standard_normal((5, e)).astype(np.float32)
+        x[1] = 0.5
+        x[2, ::2] = -INF
+        x[3, : e // 2] = -MOST
+        b = (rng.standard_normal((groups, per)) * 0.05).astype(np.float32)
+        for g in range(groups):
+            kind = rng.integers(0, 7) if draw % 2 else (0, 1, 2, 0)[g % 4]
+            if kind == 0:
+                b[g] = -INF                               # none left
+            elif kind == 1:
+                b[g] = -MOST                              # all masked by the lowest value
+            elif kind == 2:
+                b[g] = -3e38 + 1e37 * rng.integers(0, 3)  # sums beyond it, of different size
+            elif kind == 3:
+                b[g] = 3e38
+            elif kind == 4:
+                b[g, 1:] = -INF                           # one left
+            elif kind == 5:
+                b[g, ::2] = -MOST
+        bias = torch.from_numpy(b.ravel()).to(DEV)
+        verify(torch.from_numpy(x).to(DEV), min(4, topk_groups * per), sigmoid, bias, groups, topk_groups)
