@@ -4,6 +4,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <cmath>
+
 #include "checks.h"
 #include "dense.h"
 #include "gate.h"
@@ -51,7 +53,7 @@ extern "C" int ll_moe_route(int num_tokens, int num_experts, int topk, int logit
   if ((group_best != 1 && group_best != 2) || (num_groups > 1 && group_best > per)) return LL_MOE_INVALID_ARGUMENT;
   if (topk < 1 || topk > LL_MOE_MAX_TOPK || topk > topk_groups * per) return LL_MOE_INVALID_ARGUMENT;
   if (renormalize != 0 && renormalize != 1) return LL_MOE_INVALID_ARGUMENT;
-  if (!(scale >= -3.4e38f && scale <= 3.4e38f)) return LL_MOE_INVALID_ARGUMENT;
+  if (!std::isfinite(scale)) return LL_MOE_INVALID_ARGUMENT;
   if ((int64_t)num_tokens * topk > INT32_MAX) return LL_MOE_INVALID_ARGUMENT;
   if (num_tokens > 0) {
     if (!logits || !topk_idx || !topk_weights) return LL_MOE_INVALID_ARGUMENT;

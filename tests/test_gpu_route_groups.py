@@ -190,3 +190,16 @@ def test_sums_of_two_beyond_fp32(e, groups, topk_groups, sigmoid):
                 b[g, ::2] = -MOST
         bias = torch.from_numpy(b.ravel()).to(DEV)
         verify(torch.from_numpy(x).to(DEV), min(4, topk_groups * per), sigmoid, bias, groups, topk_groups)
+
+
+@pytest.mark.parametrize("sigmoid", [True, False])
+@pytest.mark.parametrize("renormalize", [True, False])
+def test_the_largest_scale(sigmoid, renormalize):
+    """Scores are at most 1, so weights stay finite."""
+    g = torch.Generator(device=DEV).manual_seed(6)
+    x = torch.randn(9, 64, generator=g, device=DEV)
+    x[1], x[2] = 0.0, -200.0
+    x[3, 5], x[4, 1:] = INF, -INF
+    for groups, topk_groups in ((8, 4), (1, 1)):
+        verify(x, 6, sigmoid, None, groups, topk_groups, 1, renormalize, MOST)
+        verify(x, 1, sigmoid, torch.zeros(64, device=DEV), groups, topk_groups, 2, renormalize, -MOST)
