@@ -203,3 +203,26 @@ def test_the_largest_scale(sigmoid, renormalize):
     for groups, topk_groups in ((8, 4), (1, 1)):
         verify(x, 6, sigmoid, None, groups, topk_groups, 1, renormalize, MOST)
         verify(x, 1, sigmoid, torch.zeros(64, device=DEV), groups, topk_groups, 2, renormalize, -MOST)
+
+
+@pytest.mark.parametrize("e,groups,topk_groups,best", [(256, 1, 1, 1), (256, 8, 4, 2), (128, 4, 2, 1), (100, 1, 1, 1),
+                                                       (64, 16, 5, 2), (512, 2, 1, 2), (96, 8, 3, 2)])
+def test_single_near_pairs_that_exist(e, groups, topk_groups, best):
+    """A pair of experts with different biases whose sigmoids with them differ
+    by some 1e-8, among the largest; biases are within 0.05, so that the scores
+    that make such a pair, 0.9 less the bias, lie between 0 and 1."""
+    rng = np.random.default_rng(e + groups)
+    rows = (rng.standard_normal((96, e)) - 1).astype(np.float32)
+    bias = (rng.standard_normal(e) * 0.02).clip(-0.05, 0.05).astype(np.float32)
+    for row in rows:
+        a, c = rng.choice(e, 2, replace=False)
+        value = 0.9 + 0.01 * rng.random()
+        for x in (a, c):
+            target = value - float(bias[x])
+            assert 0 < target < 1
+            l = np.float32(np.log(target / (1 - target)))
+            row[x] = (l.view(np.int32) + np.int32(rng.integers(-3, 4))).view(np.float32)
+    x, b = torch.from_numpy(rows).to(DEV), torch.from_numpy(bias).to(DEV)
+    assert bool(x.isfinite().all())
+    verify(x, 4, True, b, groups, topk_groups, best)
+    verify(x, 1, True, b, groups, topk_groups, best, False, 2.0)
