@@ -21,7 +21,7 @@
 // 7168, 29 MB: 8.3 us to bf16, 10.8 to fp8, of which 2.0 are the second
 // kernel and the rest its launch). Many rows: 8192 x 4096 x 7168 take 400 us, 1.2 PFLOP/s; the copies
 // alone take 203 of them and the products without copies 340, which overlap no
-// better: a SIMD's matrix unit is busy 52 % of the time, and 2.8 vector
+// better: a SIMD's matrix unit is busy 50 % of the time, and 2.8 vector
 // instructions a product (conversion and scaling) share its wavefronts' issue.
 #include <hip/hip_runtime.h>
 #include <stdint.h>

@@ -15,7 +15,7 @@
 //
 // Bound: one token 3.5 us with bf16 weights (3.7 MB) and 128 tokens 6.7
 // are latency: a launch, loads, and the sums' meeting. 16384 tokens (hidden 7168,
-// 256 experts, bf16) take 78 to 80 us, 750 to 770 TFLOP/s; their operands pass from the
+// 256 experts, bf16) take 78 to 83 us a launch, 720 to 770 TFLOP/s; their operands pass from the
 // caches to LDS at 12 TB/s, and each SIMD's one or two wavefronts wait for each
 // other at every step.
 #include <hip/hip_runtime.h>
@@ -128,8 +128,8 @@ __global__ void __launch_bounds__(64) gate_row_kernel(const GateParams P) {
 
 // 16 tokens x EW experts (as few as the GPU has room for). fp32 weights are
 // cut on their way into LDS, once each (cut as fragments, whose 16 rows repeat
-// the EW, 128 tokens by 256 experts took 11.2 us, as it is 10.7, and with loads
-// one step ahead instead of two 9.2: fewer registers, more wavefronts).
+// the EW, 128 tokens by 256 experts took 11.2 us, cut once with loads two steps
+// ahead 10.7, and one step ahead, as it is, 9.2: fewer registers, more wavefronts).
 template <bool FP32, int EW, int WAVES>
 __global__ void __launch_bounds__(WAVES * 64) gate_few_kernel(const GateParams P) {
   constexpr int ITEM = FP32 ? 4 : 2, WROW = kColumns * ITEM, WL = (EW * WROW + 1023) / 1024;
@@ -385,15 +385,16 @@ hipError_t launch_row(const GateParams& p, hipStream_t stream) {
 
 }  // namespace
 
-// Which kernel, by the sizes (us at hidden 7168 and 256 experts, weights bf16 |
-// fp32). Up to kRowTokens tokens: a wavefront an expert (1 token 3.5 | 4.2, where
-// 16 x 8 take 6.0 | 9.6; 4 tokens 6.1 | 6.5 against 6.0 | 9.8). Then 16 tokens
-// by as few experts as fill the GPU once (64 tokens: 16 x 4 6.3 | 8.2, 16 x 8 6.4 |
-// 8.9, 16 x 16 7.7 | 11.2; 128 tokens 10.4 | 13.5, 6.7 | 9.2, 7.9 | 11.4; 256 tokens
-// 16 x 16 8.4 | 12.1), more than 256 of those with eight wavefronts (512 tokens 13.2 |
-// 21.6, with sixteen 13.7 | 22.4), up to as many logits as tiles do faster (768
-// tokens 18.7 against 21.3, 1024 tokens 27 against 24 | 44 against 48). Then the smallest tiles that are
-// not too many: 64 x 32 (2048 tokens 30 | 51, in 64 x 64 34 | 79; 4096 tokens 50 |
+// Which kernel, by the sizes (us a launch in a row of launches, operands out of the
+// caches, all at hidden 7168 and 256 experts, weights bf16 | fp32). Up to kRowTokens
+// tokens: a wavefront an expert (1 token 3.5 | 4.2, where 16 x 8 take 6.0 | 9.6; 4 tokens
+// 6.1 | 6.5 against 6.0 | 9.8). Then 16 tokens by as few experts as fill the GPU once, 4
+// with fp32 weights alone (64 tokens: 16 x 4
+// 6.3 | 8.2, 16 x 8 6.4 | 8.9, 16 x 16 7.7 | 11.2; 128 tokens 10.4 | 13.5, 6.7 | 9.2, 7.9 |
+// 11.4; 256 tokens 16 x 16 8.4 | 12.1), more than 256 of those with eight wavefronts (512
+// tokens 13.2 | 21.6, with sixteen 13.7 | 22.4), up to as many logits as tiles do faster
+// (768 tokens 18.7 against 21.3, 1024 tokens 27 against 24 | 44 against 48). Then the
+// smallest tiles that are not too many: 64 x 32 (2048 tokens 30 | 51, in 64 x 64 34 | 79; 4096 tokens 50 |
 // 77), then with bf16 64 x 64 (4096 tokens 36; 8192 63), 64 x 128, two a CU (4096
 // tokens 52, 8192 54, 10000 96), and 128 x 128 (8192 tokens 70, 10000 71, 16384
 // 78), with fp32 128 x 32 (4096 tokens 93, 8192 110, 16384 216) and 128 x 64
